@@ -380,6 +380,106 @@ NVFP4_API nvfp4_status gather_qmm_noalloc(const void* x, const uint32_t* w_codes
                                           const float* g, const int32_t* idx, int64_t T, int64_t topk,
                                           int64_t E, int64_t N, int64_t K, void* y, nvfp4_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged key/value cache held in NVFP4, MXFP8 or MXFP4, and attention over it.
+ * (No page counterpart: the formats and the per-block arithmetic are those
+ * of the quantizers above; the cache layout is this library's.)
+ *
+ * A cache holds num_pages pages of page_size rows for each of `heads`
+ * key/value heads of D elements:
+ *   k_codes, v_codes   [num_pages, heads, page_size, D/8] uint32 (MXFP8: D/4)
+ *   k_scales, v_scales [num_pages, heads, page_size, D/16] e4m3 bytes (NVFP4)
+ *                      or D/32 e8m0 bytes (the MX modes), LINEAR.
+ * Slot s is row s % page_size of page s / page_size.  A contiguous
+ * [B, heads, L, D] cache is the case num_pages = B, page_size = L.
+ * g_k, g_v: global scales of the two sides (NVFP4 only; both or neither),
+ * fixed for the cache's life: blocks beyond them saturate.
+ * D % 32 == 0 and 32 <= D <= 256 (beyond: NVFP4_ERR_UNSUPPORTED);
+ * heads <= 65535; page_size >= 1; num_pages * page_size < 2^31 (byte offsets
+ * are 64-bit).  Rows that were never written may hold any bytes: no call
+ * reads a row its arguments do not name.
+ * The struct is read on the host during the call. */
+typedef struct {
+  nvfp4_mode mode;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t heads;
+  int64_t D;
+  uint32_t* k_codes;
+  uint8_t* k_scales;
+  uint32_t* v_codes;
+  uint8_t* v_scales;
+  const float* g_k;
+  const float* g_v;
+} nvfp4_kv_cache;
+
+/* kv_cache_write -- quantize the keys and values of T tokens into their slots
+ * (one launch): every row gets exactly the codes and scales nvfp4_quantize,
+ * mxfp8_quantize or mxfp4_quantize would give it (LINEAR).  Other rows are
+ * left as they are.
+ * k, v [T, heads, D] of dt (fp32, fp16, bf16): heads and D contiguous, tokens
+ * k_stride and v_stride elements apart (>= heads*D, or any value for T <= 1;
+ * a multiple of 16 bytes), so both may be parts of one projection's rows.
+ * slots [T] int32: a negative slot skips its token; a slot past the cache
+ * skips it and sets NVFP4_ERR_DEVICE_INDEX.  The slots of one call must
+ * differ (which token's bytes a repeated slot ends with is unspecified).
+ * T*heads*D at most 2^34. */
+NVFP4_API nvfp4_status kv_cache_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
+                                      int64_t T, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                      nvfp4_stream_t stream);
+
+/* kv_cache_read -- the values of T slots (one launch), exactly as
+ * nvfp4_dequantize, mxfp8_dequantize or mxfp4_dequantize give them:
+ * k_out, v_out [T, heads, D] of out_dt, contiguous.  A negative slot gives a
+ * zero row; a slot past the cache a zero row and NVFP4_ERR_DEVICE_INDEX.
+ * Slots may repeat.  T*heads*D at most 2^34. */
+NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t T, void* k_out,
+                                     void* v_out, nvfp4_dtype out_dt, nvfp4_stream_t stream);
+
+/* kv_attention -- attention of B sequences' queries over their cached tokens,
+ * for single new tokens and for prompts alike.  Token j of sequence b is row
+ * j % page_size of page page_table[b, j / page_size].  Query i of the n
+ * queries of a sequence with L = kv_len[b] cached tokens (those of the
+ * queries included) is at position p = L - n + i and sees token j iff j < L,
+ * j <= p when causal, and j > p - window when window > 0:
+ *   z_j = scale * q . k_hat_j,  out = sum_j softmax(z)_j v_hat_j,
+ *   lse = ln(sum_j exp(z_j)),
+ * with k_hat, v_hat the cache's exact values (code * block scale * g/2688;
+ * not rounded to q's type), fp32 sums and statistics.  A query that sees
+ * nothing gets out = 0 and lse = -infinity.  Query head h reads key/value
+ * head h / (Hq / heads).
+ * q: fp16 or bf16, [T, Hq, D], heads and D contiguous, tokens q_stride
+ * elements apart (>= Hq*D, or any value for T <= 1; a multiple of 16 bytes).
+ * q_start [B+1] int32: the queries of sequence b are tokens q_start[b] ..
+ * q_start[b+1]-1 (0 <= q_start[b] <= q_start[b+1] <= T, at most max_q of
+ * them); NULL: one query a sequence, token b (T == B, max_q == 1).
+ * kv_len [B] int32, each in [0, max_kv]; page_table [B, max_pages] int32,
+ * entries the sequence needs in [0, num_pages) (others are not read as
+ * pages); 0 <= max_kv <= max_pages*page_size.  max_q and max_kv are host
+ * bounds: they choose the launch, so tight ones are faster.
+ * out [T, Hq, D] of q's type; lse [T, Hq] fp32 or NULL.  Rows of out and lse
+ * that no sequence names are left as they are.
+ * A sequence whose entries break these bounds is skipped (its rows left as
+ * they are), and a token on a page out of range counts as unseen; both set
+ * NVFP4_ERR_DEVICE_INDEX.
+ * MX modes: a value block's scale above 2^64 counts as 2^64.
+ * Hq a multiple of heads, Hq <= 65535; B <= 65535; T*Hq*D at most 2^34.
+ * workspace: device scratch, 16-byte aligned, contents undefined on entry
+ * and exit; with at least kv_attention_workspace_size bytes long sequences
+ * are split over the SMs and joined, with less (NULL, 0 included) they are
+ * split less or not at all.  Calls that may overlap need one each. */
+NVFP4_API nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
+                                    const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                    int64_t B, int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv,
+                                    int64_t max_pages, float scale, int causal, int64_t window, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Bytes of workspace with which kv_attention splits as it would choose to,
+ * for a cache of `heads` heads of D; 0 when it would not split (or for sizes
+ * it rejects).  Host only. */
+NVFP4_API size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D,
+                                             int64_t max_q, int64_t max_kv, int64_t window);
+
 #ifdef __cplusplus
 }
 #endif

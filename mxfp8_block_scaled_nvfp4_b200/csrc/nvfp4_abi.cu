@@ -18,6 +18,8 @@
 #include "qmv_tc.cuh"
 #include "qqmm_sm100.cuh"
 #include "gather_qmm.cuh"
+#include "kv_cache.cuh"
+#include "kv_attention.cuh"
 
 using namespace nvfp4;
 
@@ -128,6 +130,15 @@ void dispatch_dt(nvfp4_dtype dt, F&& f) {
     case NVFP4_DT_F32: f(float{}); break;
     case NVFP4_DT_F16: f(__half{}); break;
     default: f(__nv_bfloat16{}); break;
+  }
+}
+
+template <typename F>
+void dispatch_mode(nvfp4_mode mode, F&& f) {
+  switch (mode) {
+    case NVFP4_MODE_NVFP4: f(std::integral_constant<int, kv::kNV>{}); break;
+    case NVFP4_MODE_MXFP8: f(std::integral_constant<int, kv::kMX8>{}); break;
+    default: f(std::integral_constant<int, kv::kMX4>{}); break;
   }
 }
 
@@ -796,6 +807,204 @@ nvfp4_status gather_qmm_noalloc(const void* x, const uint32_t* w_codes, const ui
   // (tile count, tile list, permutation; the staging kernel the staged rows
   // of every routed pair), so nothing needs clearing between calls.
   return gather_qmm(x, w_codes, w_scales, g, idx, T, topk, E, N, K, y, scratch, kNoAllocScratchBytes, stream);
+}
+
+// Checks of a cache handle that every cache call makes.
+static nvfp4_status check_kv_cache(const char* tag, const nvfp4_kv_cache* c) {
+  if (!c) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null cache", tag);
+  if (c->mode != NVFP4_MODE_NVFP4 && c->mode != NVFP4_MODE_MXFP8 && c->mode != NVFP4_MODE_MXFP4)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] mode must be 'nvfp4', 'mxfp8' or 'mxfp4'", tag);
+  if (c->mode != NVFP4_MODE_NVFP4 && (c->g_k || c->g_v))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] Global scales are only supported for 'nvfp4' mode.", tag);
+  if ((c->g_k == nullptr) != (c->g_v == nullptr))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] either both g_k and g_v must be provided, or neither.", tag);
+  if (c->num_pages < 0 || c->page_size < 1 || product_exceeds(c->num_pages, c->page_size, INT32_MAX) ||
+      c->page_size > INT32_MAX)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad cache of %lld pages of %lld rows (fewer than 2^31 rows in all)", tag,
+                (long long)c->num_pages, (long long)c->page_size);
+  if (c->heads < 1 || c->heads > 65535)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] heads must be in [1, 65535], got %lld", tag, (long long)c->heads);
+  if (c->D < 32 || c->D % 32 != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] D must be a positive multiple of 32, got %lld", tag, (long long)c->D);
+  if (c->D > 256) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] D must be at most 256, got %lld", tag, (long long)c->D);
+  if (c->num_pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] null cache pointer", tag);
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales) ||
+      (reinterpret_cast<uintptr_t>(c->g_k) & 3u) || (reinterpret_cast<uintptr_t>(c->g_v) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned", tag);
+  return NVFP4_OK;
+}
+
+static int64_t dt_size(nvfp4_dtype dt) { return dt == NVFP4_DT_F32 ? 4 : 2; }
+
+// Token stride of a [T, width] operand whose rows may be parts of longer ones.
+static bool bad_stride(int64_t T, int64_t stride, int64_t width, nvfp4_dtype dt) {
+  return T > 1 && (stride < width || stride > INT32_MAX || stride * dt_size(dt) % 16 != 0);
+}
+
+static kv::RowArgs kv_row_args(const nvfp4_kv_cache* c, int64_t T, const int32_t* slots) {
+  kv::RowArgs a;
+  memset(&a, 0, sizeof(a));
+  a.codes[0] = reinterpret_cast<uint8_t*>(c->k_codes);
+  a.codes[1] = reinterpret_cast<uint8_t*>(c->v_codes);
+  a.scales[0] = c->k_scales;
+  a.scales[1] = c->v_scales;
+  a.g[0] = c->g_k;
+  a.g[1] = c->g_v;
+  a.slots = slots;
+  a.T = (uint32_t)T;
+  a.heads = (uint32_t)c->heads;
+  a.D = (uint32_t)c->D;
+  a.page_size = (uint32_t)c->page_size;
+  a.num_slots = (uint32_t)(c->num_pages * c->page_size);
+  a.units = (uint32_t)(T * c->heads * c->D / 16);
+  a.per_head.init(a.D / 16u);
+  a.per_token.init(a.heads * (a.D / 16u));
+  a.by_page.init(a.page_size);
+  return a;
+}
+
+nvfp4_status kv_cache_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt, int64_t T,
+                            int64_t k_stride, int64_t v_stride, const int32_t* slots, nvfp4_stream_t stream) {
+  const char* tag = "kv_cache_write";
+  nvfp4_status st = check_kv_cache(tag, cache);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dt(dt)) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] dtype must be float32, float16 or bfloat16", tag);
+  const int64_t width = cache->heads * cache->D;
+  if (T < 0 || product_exceeds(T, width, kMaxElems)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad T=%lld", tag, (long long)T);
+  if (bad_stride(T, k_stride, width, dt) || bad_stride(T, v_stride, width, dt))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] token strides must be at least heads*D and a multiple of 16 bytes", tag);
+  if (T > 0 && (!k || !v || !slots)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned (slots 4-byte)", tag);
+  if (T == 0) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  kv::RowArgs a = kv_row_args(cache, T, slots);
+  a.x[0] = k;
+  a.x[1] = v;
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  const dim3 grid((a.units + kv::kRowThreads - 1) / kv::kRowThreads, 2);
+  dispatch_dt(dt, [&](auto tag_t) {
+    using E = decltype(tag_t);
+    dispatch_mode(cache->mode, [&](auto m) { kv::k_kv_write<E, decltype(m)::value><<<grid, kv::kRowThreads, 0, stream>>>(a); });
+  });
+  return check_launch(tag);
+}
+
+nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t T, void* k_out, void* v_out,
+                           nvfp4_dtype out_dt, nvfp4_stream_t stream) {
+  const char* tag = "kv_cache_read";
+  nvfp4_status st = check_kv_cache(tag, cache);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dt(out_dt)) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] dtype must be float32, float16 or bfloat16", tag);
+  const int64_t width = cache->heads * cache->D;
+  if (T < 0 || product_exceeds(T, width, kMaxElems)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad T=%lld", tag, (long long)T);
+  if (T > 0 && (!k_out || !v_out || !slots)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (!aligned16(k_out) || !aligned16(v_out) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned (slots 4-byte)", tag);
+  if (T == 0) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  kv::RowArgs a = kv_row_args(cache, T, slots);
+  a.x[0] = k_out;
+  a.x[1] = v_out;
+  a.stride[0] = a.stride[1] = width;
+  const dim3 grid((a.units + kv::kRowThreads - 1) / kv::kRowThreads, 2);
+  dispatch_dt(out_dt, [&](auto tag_t) {
+    using E = decltype(tag_t);
+    dispatch_mode(cache->mode, [&](auto m) { kv::k_kv_read<E, decltype(m)::value><<<grid, kv::kRowThreads, 0, stream>>>(a); });
+  });
+  return check_launch(tag);
+}
+
+size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q,
+                                   int64_t max_kv, int64_t window) {
+  (void)B, (void)T, (void)Hq, (void)heads, (void)D, (void)max_q, (void)max_kv, (void)window;
+  return 0;
+}
+
+nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
+                          const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int64_t B,
+                          int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv, int64_t max_pages, float scale,
+                          int causal, int64_t window, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                          nvfp4_stream_t stream) {
+  const char* tag = "kv_attention";
+  nvfp4_status st = check_kv_cache(tag, cache);
+  if (st != NVFP4_OK) return st;
+  if (q_dt != NVFP4_DT_F16 && q_dt != NVFP4_DT_BF16)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] q must be float16 or bfloat16", tag);
+  if (B < 0 || B > 65535 || T < 0 || T > (1 << 30) || Hq < 1 || Hq > 65535 || max_q < 0 || max_q > (1 << 30) ||
+      max_pages < 0 || max_pages > INT32_MAX)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad sizes B=%lld T=%lld Hq=%lld max_q=%lld max_pages=%lld", tag,
+                (long long)B, (long long)T, (long long)Hq, (long long)max_q, (long long)max_pages);
+  if (Hq % cache->heads != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] Hq must be a multiple of the cache's heads, got %lld and %lld", tag,
+                (long long)Hq, (long long)cache->heads);
+  if (product_exceeds(T, Hq * cache->D, kMaxElems))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] T*Hq*D must be at most 2^34", tag);
+  if (max_kv < 0 || max_kv > INT32_MAX || (max_kv > 0 && (max_pages == 0 || (max_kv - 1) / cache->page_size >= max_pages)))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_kv must be in [0, max_pages*page_size], got %lld", tag, (long long)max_kv);
+  if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "[%s] window must not be negative", tag);
+  if (!q_start && (T != B || max_q != 1))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] without q_start, T must equal B and max_q be 1", tag);
+  if (!(scale - scale == 0.0f)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] scale must be finite", tag);
+  if (bad_stride(T, q_stride, Hq * cache->D, q_dt))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] the token stride must be at least Hq*D and a multiple of 16 bytes", tag);
+  const bool empty = T == 0 || B == 0 || max_q == 0;
+  if (!empty && (!q || !out || !kv_len || (max_pages > 0 && !page_table)))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (workspace_bytes > 0 && !workspace) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null workspace", tag);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(q_start) & 3u) || (reinterpret_cast<uintptr_t>(kv_len) & 3u) ||
+      (reinterpret_cast<uintptr_t>(page_table) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] q, out and workspace must be 16-byte aligned (lse and the index arrays 4-byte)", tag);
+  if (empty) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  kv::AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.codes[0] = reinterpret_cast<const uint8_t*>(cache->k_codes);
+  a.codes[1] = reinterpret_cast<const uint8_t*>(cache->v_codes);
+  a.scales[0] = cache->k_scales;
+  a.scales[1] = cache->v_scales;
+  a.g[0] = cache->g_k;
+  a.g[1] = cache->g_v;
+  a.q = q;
+  a.q_stride = T > 1 ? q_stride : Hq * cache->D;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.out = out;
+  a.lse = lse;
+  a.scale = scale;
+  a.B = (uint32_t)B;
+  a.T = (uint32_t)T;
+  a.Hq = (uint32_t)Hq;
+  a.heads = (uint32_t)cache->heads;
+  a.G = (uint32_t)(Hq / cache->heads);
+  a.D = (uint32_t)cache->D;
+  a.max_q = (uint32_t)max_q;
+  a.max_kv = (uint32_t)max_kv;
+  a.max_pages = (uint32_t)max_pages;
+  a.num_pages = (uint32_t)cache->num_pages;
+  a.page_size = (uint32_t)cache->page_size;
+  a.window = window > INT32_MAX ? 0u : (uint32_t)window;  // a window past any length hides nothing
+  a.causal = causal != 0;
+  a.by_page.init(a.page_size);
+  const dim3 grid((unsigned)max_q, (unsigned)Hq, (unsigned)B);
+  dispatch_mode(cache->mode, [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
+    if (q_dt == NVFP4_DT_F16)
+      kv::k_kv_attention<__half, MODE><<<grid, kv::kPlainWarps * 32, 0, stream>>>(a);
+    else
+      kv::k_kv_attention<__nv_bfloat16, MODE><<<grid, kv::kPlainWarps * 32, 0, stream>>>(a);
+  });
+  return check_launch(tag);
 }
 
 }  // extern "C"

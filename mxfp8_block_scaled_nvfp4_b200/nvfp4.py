@@ -39,6 +39,12 @@ class QuantizeItem(ctypes.Structure):
                 ("layout", _I)]
 
 
+class KvCacheArgs(ctypes.Structure):
+    """nvfp4_kv_cache"""
+    _fields_ = [("mode", _I), ("num_pages", _I64), ("page_size", _I64), ("heads", _I64), ("D", _I64),
+                ("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("g_k", _P), ("g_v", _P)]
+
+
 SIGNATURES = [
     ("nvfp4_status_string", ctypes.c_char_p, [_I]),
     ("nvfp4_last_error_message", ctypes.c_char_p, []),
@@ -66,6 +72,11 @@ SIGNATURES = [
     ("gather_qmm_workspace_size", _SZ, [_I64, _I64, _I64]),
     ("gather_qmm_staged_workspace_size", _SZ, [_I64, _I64, _I64, _I64]),
     ("gather_qmm_noalloc", _I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P]),
+    ("kv_cache_write", _I, [ctypes.POINTER(KvCacheArgs), _P, _P, _I, _I64, _I64, _I64, _P, _P]),
+    ("kv_cache_read", _I, [ctypes.POINTER(KvCacheArgs), _P, _I64, _P, _P, _I, _P]),
+    ("kv_attention", _I, [ctypes.POINTER(KvCacheArgs), _P, _I, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                          ctypes.c_float, _I, _I64, _P, _P, _P, _SZ, _P]),
+    ("kv_attention_workspace_size", _SZ, [_I64] * 8),
 ]
 
 _lib = None
@@ -519,3 +530,163 @@ def gather_qmm_noalloc(x, w_codes, w_scales, g, idx, out=None) -> torch.Tensor:
     _check(lib().gather_qmm_noalloc(_ptr(x), _ptr(w_codes), _ptr(w_scales), _ptr(g), _ptr(idx), T, topk, E, N, K,
                                     _ptr(out), _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------
+# key/value cache
+# ---------------------------------------------------------------------------
+class KvCache:
+    """Handle of a paged key/value cache (nvfp4_kv_cache): the caller's tensors
+    and the sizes they hold.  codes int32 [num_pages, heads, page_size, D/8]
+    (D/4 for "mxfp8"), scales uint8 [num_pages, heads, page_size, D/16]
+    ("nvfp4") or D/32; g_k, g_v fp32 [1] or None ("nvfp4" only, both or
+    neither).  The handle keeps references to the tensors and no copy."""
+
+    def __init__(self, mode: str, k_codes, k_scales, v_codes, v_scales, g_k=None, g_v=None):
+        if mode not in MODE:
+            raise ValueError("KvCache: mode must be nvfp4, mxfp8 or mxfp4")
+        if k_codes.dim() != 4:
+            raise ValueError("KvCache: codes must be [num_pages, heads, page_size, words]")
+        P, H, R, words = k_codes.shape
+        D = words * (4 if mode == "mxfp8" else 8)
+        sshape = (P, H, R, D // (16 if mode == "nvfp4" else 32))
+        for t, what, dtype, shape in ((k_codes, "k_codes", torch.int32, k_codes.shape),
+                                      (v_codes, "v_codes", torch.int32, k_codes.shape),
+                                      (k_scales, "k_scales", torch.uint8, sshape),
+                                      (v_scales, "v_scales", torch.uint8, sshape)):
+            _need_dtype(t, dtype, what)
+            if tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+        _need_g(g_k, 1, "g_k")
+        _need_g(g_v, 1, "g_v")
+        _need_cuda(k_codes, k_scales, v_codes, v_scales, g_k, g_v)
+        self.mode, self.num_pages, self.heads, self.page_size, self.D = mode, P, H, R, D
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.g_k, self.g_v = g_k, g_v
+        self.device = k_codes.device
+        self._args = KvCacheArgs(MODE[mode], P, R, H, D, *(None if t is None else t.data_ptr() for t in (
+            k_codes, k_scales, v_codes, v_scales, g_k, g_v)))
+        self._ref = ctypes.byref(self._args)
+
+    @classmethod
+    def empty(cls, mode: str, num_pages: int, heads: int, page_size: int, D: int, g_k=None, g_v=None, device="cuda"):
+        """A cache in new tensors (contents undefined until written)."""
+        if mode not in MODE:
+            raise ValueError("KvCache: mode must be nvfp4, mxfp8 or mxfp4")
+        t = []
+        for _ in range(2):
+            t.append(torch.empty(num_pages, heads, page_size, D // (4 if mode == "mxfp8" else 8), dtype=torch.int32,
+                                 device=device))
+            t.append(torch.empty(num_pages, heads, page_size, D // (16 if mode == "nvfp4" else 32), dtype=torch.uint8,
+                                 device=device))
+        return cls(mode, *t, g_k, g_v)
+
+
+def _need_rows(t, shape, what: str):
+    """[T, heads, D] on the current device, heads and D contiguous, any token
+    stride (a part of a longer row is taken as it is)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} on {t.device}, but the current device is cuda:{torch.cuda.current_device()}; "
+                         "call under torch.cuda.device(tensor.device)")
+    if t.numel() and ((t.stride(2) != 1 and shape[2] > 1) or (t.stride(1) != shape[2] and shape[1] > 1)):
+        raise ValueError(f"{what}: heads and D must be contiguous")
+
+
+def _need_cache(cache):
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device(cache.device)")
+
+
+def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize k, v [T, heads, D] (one dtype; any token stride) into the
+    cache's slots [T] int32 (negative: skipped)."""
+    shape = (slots.shape[0], cache.heads, cache.D)
+    if k.dtype != v.dtype or k.dtype not in DT:
+        raise ValueError("k and v must share a dtype: float32, float16 or bfloat16")
+    _need_dtype(slots, torch.int32, "slots")
+    _need_cuda(slots)
+    _need_cache(cache)
+    _need_rows(k, shape, "k")
+    _need_rows(v, shape, "v")
+    _check(lib().kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), DT[k.dtype], shape[0], k.stride(0),
+                                v.stride(0), slots.data_ptr(), _stream()))
+
+
+def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None):
+    """(k, v) [T, heads, D]: the values of the slots [T] int32 (negative: zero
+    rows)."""
+    shape = (slots.shape[0], cache.heads, cache.D)
+    _need_dtype(slots, torch.int32, "slots")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=slots.device)
+    if k_out.dtype != v_out.dtype or k_out.dtype not in DT:
+        raise ValueError("k_out and v_out must share a dtype: float32, float16 or bfloat16")
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
+    _need_cuda(slots, k_out, v_out)
+    _need_cache(cache)
+    _check(lib().kv_cache_read(cache._ref, slots.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(),
+                               DT[k_out.dtype], _stream()))
+    return k_out, v_out
+
+
+def kv_attention_workspace_size(B: int, T: int, Hq: int, heads: int, D: int, max_q: int = 1, max_kv: int = 0,
+                                window: int = 0) -> int:
+    return int(lib().kv_attention_workspace_size(B, T, Hq, heads, D, max_q, max_kv, window))
+
+
+def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                 q_start: torch.Tensor | None = None, max_q: int | None = None, max_kv: int | None = None,
+                 scale: float | None = None, causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """out [T, Hq, D] (q's dtype) = attention of the queries q [T, Hq, D] (fp16
+    or bf16) over the cached tokens of their sequences; with return_lse (or an
+    lse tensor [T, Hq] fp32) the pair (out, lse).
+    page_table [B, max_pages] int32, kv_len [B] int32 (the queries' own tokens
+    included).  q_start [B + 1] int32: sequence b has tokens q_start[b] ..
+    q_start[b + 1] - 1 (None: one query a sequence).  max_q, max_kv: host
+    bounds on queries and cached tokens of a sequence (default: T and all of
+    the page table; tight bounds are faster).  scale defaults to D ** -0.5.
+    workspace: uint8 scratch of kv_attention_workspace_size bytes (allocated
+    here when None)."""
+    T, Hq = q.shape[0], q.shape[1]
+    B, max_pages = page_table.shape
+    _need_dtype(page_table, torch.int32, "page_table")
+    _need_dtype(kv_len, torch.int32, "kv_len")
+    _need_bytes(kv_len, 4 * B, "kv_len")
+    _need_dtype(q_start, torch.int32, "q_start")
+    _need_bytes(q_start, 4 * (B + 1), "q_start")
+    _need_dtype(out, q.dtype, "out")
+    _need_bytes(out, T * Hq * cache.D * q.element_size(), "out")
+    _need_dtype(lse, torch.float32, "lse")
+    _need_bytes(lse, 4 * T * Hq, "lse")
+    _need_cuda(page_table, kv_len, q_start, out, lse, workspace)
+    _need_cache(cache)
+    _need_rows(q, (T, Hq, cache.D), "q")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
+    if max_q is None:
+        max_q = 1 if q_start is None else T
+    if max_kv is None:
+        max_kv = max_pages * cache.page_size
+    if out is None:
+        out = torch.empty(T, Hq, cache.D, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    L = lib()
+    if workspace is None:
+        size = L.kv_attention_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    _check(L.kv_attention(cache._ref, q.data_ptr(), DT[q.dtype], q.stride(0), _ptr(q_start), kv_len.data_ptr(),
+                          page_table.data_ptr(), B, T, Hq, max_q, max_kv, max_pages,
+                          cache.D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(), _ptr(lse),
+                          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream()))
+    return out if lse is None else (out, lse)
