@@ -455,14 +455,14 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  * them); NULL: one query a sequence, token b (T == B, max_q == 1).
  * kv_len [B] int32, each in [0, max_kv]; page_table [B, max_pages] int32,
  * entries the sequence needs in [0, num_pages) (others are not read as
- * pages); 0 <= max_kv <= max_pages*page_size.  max_q and max_kv are host
+ * pages); 0 <= max_kv <= max_pages*page_size, max_kv <= 2^30.  max_q and max_kv are host
  * bounds: they choose the launch, so tight ones are faster.
  * out [T, Hq, D] of q's type; lse [T, Hq] fp32 or NULL.  Rows of out and lse
  * that no sequence names are left as they are.
  * A sequence whose entries break these bounds is skipped (its rows left as
  * they are), and a token on a page out of range counts as unseen; both set
  * NVFP4_ERR_DEVICE_INDEX.
- * MX modes: a value block's scale above 2^64 counts as 2^64.
+ * MX modes: a block scale above 2^64 counts as 2^64.
  * Hq a multiple of heads, Hq <= 65535; B <= 65535; T*Hq*D at most 2^34.
  * workspace: device scratch, 16-byte aligned, contents undefined on entry
  * and exit; with at least kv_attention_workspace_size bytes long sequences

@@ -921,10 +921,40 @@ nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
   return check_launch(tag);
 }
 
+// How kv_attention cuts its work: rows of queries a CTA holds, tokens a CTA
+// walks and the largest number of such chunks a row tile can have.
+struct KvPlan {
+  int64_t tile_rows, chunk, chunks, bytes_per_chunk;
+};
+static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
+                      int64_t window, size_t workspace_bytes) {
+  KvPlan p;
+  const int64_t rows = max_q * (Hq / heads);
+  p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;
+  p.bytes_per_chunk = T * Hq * (D * 4 + 8);
+  // tokens a tile's range can span, from a multiple of 16
+  int64_t span = max_kv;
+  if (window > 0 && window + max_q + 30 < span) span = window + max_q + 30;
+  const double tiles = (double)B * (double)heads * (double)((rows + p.tile_rows - 1) / p.tile_rows);
+  const double share = (double)span * tiles / (148 * 6);  // may exceed 64-bit integers
+  int64_t chunk = share < (double)span ? (int64_t)share + 1 : span;
+  int64_t fit = workspace_bytes == SIZE_MAX ? span : (int64_t)(workspace_bytes / (size_t)p.bytes_per_chunk);
+  if (fit < 2) fit = 1;
+  if ((span + fit - 1) / fit > chunk) chunk = (span + fit - 1) / fit;
+  p.chunk = (chunk + 127) / 128 * 128;
+  if (p.chunk < 128) p.chunk = 128;
+  p.chunks = span > 0 ? (span + p.chunk - 1) / p.chunk : 1;
+  return p;
+}
+
 size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q,
                                    int64_t max_kv, int64_t window) {
-  (void)B, (void)T, (void)Hq, (void)heads, (void)D, (void)max_q, (void)max_kv, (void)window;
-  return 0;
+  if (B < 1 || B > 65535 || T < 1 || T > (1 << 30) || heads < 1 || heads > 65535 || Hq < 1 || Hq > 65535 ||
+      Hq % heads != 0 || D < 32 || D > 256 || D % 32 != 0 || max_q < 1 || max_q > (1 << 30) || max_kv < 0 ||
+      max_kv > (1 << 30) || window < 0 || product_exceeds(T, Hq * D, kMaxElems))
+    return 0;
+  const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, SIZE_MAX);
+  return p.chunks > 1 ? (size_t)(p.chunks * p.bytes_per_chunk) : 0;
 }
 
 nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
@@ -946,7 +976,8 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
                 (long long)Hq, (long long)cache->heads);
   if (product_exceeds(T, Hq * cache->D, kMaxElems))
     return fail(NVFP4_ERR_INVALID_ARG, "[%s] T*Hq*D must be at most 2^34", tag);
-  if (max_kv < 0 || max_kv > INT32_MAX || (max_kv > 0 && (max_pages == 0 || (max_kv - 1) / cache->page_size >= max_pages)))
+  if (max_kv > (1 << 30)) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] max_kv must be at most 2^30", tag);
+  if (max_kv < 0 || (max_kv > 0 && (max_pages == 0 || (max_kv - 1) / cache->page_size >= max_pages)))
     return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_kv must be in [0, max_pages*page_size], got %lld", tag, (long long)max_kv);
   if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "[%s] window must not be negative", tag);
   if (!q_start && (T != B || max_q != 1))
@@ -993,16 +1024,41 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.max_pages = (uint32_t)max_pages;
   a.num_pages = (uint32_t)cache->num_pages;
   a.page_size = (uint32_t)cache->page_size;
-  a.window = window > INT32_MAX ? 0u : (uint32_t)window;  // a window past any length hides nothing
+  a.window = window > (1 << 30) ? 0u : (uint32_t)window;  // a window past any length hides nothing
   a.causal = causal != 0;
   a.by_page.init(a.page_size);
-  const dim3 grid((unsigned)max_q, (unsigned)Hq, (unsigned)B);
+  const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, workspace_bytes);
+  a.chunk = (int32_t)p.chunk;
+  a.chunks = (uint32_t)p.chunks;
+  a.tile_rows = (uint32_t)p.tile_rows;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (size_t)p.chunks * T * Hq * cache->D * 4);
+  const int64_t tiles = (max_q * a.G + p.tile_rows - 1) / p.tile_rows;
+  if (product_exceeds(tiles, p.chunks, INT32_MAX)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q and max_kv too large", tag);
+  const dim3 grid((unsigned)(tiles * p.chunks), a.heads, a.B);
+  const bool p16 = a.page_size % 16 == 0;
   dispatch_mode(cache->mode, [&](auto m) {
     constexpr int MODE = decltype(m)::value;
-    if (q_dt == NVFP4_DT_F16)
-      kv::k_kv_attention<__half, MODE><<<grid, kv::kPlainWarps * 32, 0, stream>>>(a);
-    else
-      kv::k_kv_attention<__nv_bfloat16, MODE><<<grid, kv::kPlainWarps * 32, 0, stream>>>(a);
+    auto with_type = [&](auto t) {
+      using QT = decltype(t);
+      auto with_dim = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        auto go = [&](auto kern) { kern<<<grid, kv::kDecThreads, 0, stream>>>(a); };
+        if constexpr (DP <= 128) {
+          if (p.tile_rows == 16) {
+            p16 ? go(kv::k_kv_decode<QT, MODE, DP, 2, true>) : go(kv::k_kv_decode<QT, MODE, DP, 2, false>);
+            return;
+          }
+        }
+        p16 ? go(kv::k_kv_decode<QT, MODE, DP, 1, true>) : go(kv::k_kv_decode<QT, MODE, DP, 1, false>);
+      };
+      if (a.D <= 64) with_dim(std::integral_constant<int, 64>{});
+      else if (a.D <= 128) with_dim(std::integral_constant<int, 128>{});
+      else with_dim(std::integral_constant<int, 256>{});
+      if (p.chunks > 1) kv::k_kv_join<QT><<<dim3(a.max_q, a.Hq, a.B), kv::kJoinWarps * 32, 0, stream>>>(a);
+    };
+    if (q_dt == NVFP4_DT_F16) with_type(__half{});
+    else with_type(__nv_bfloat16{});
   });
   return check_launch(tag);
 }

@@ -88,6 +88,7 @@ def test_attention_arguments(L):
     assert attend(L, c, T=3) == 1 and "q_start" in msg(L)
     assert attend(L, c, max_q=2) == 1
     assert attend(L, c, max_kv=65) == 1 and "max_kv" in msg(L)
+    assert attend(L, cache(page_size=1 << 20), max_kv=(1 << 30) + 1, max_pages=2048) == 2 and "2^30" in msg(L)
     assert attend(L, c, max_kv=-1) == 1 and attend(L, c, window=-1) == 1
     assert attend(L, c, scale=INF) == 1 and attend(L, c, scale=float("nan")) == 1
     assert attend(L, c, stride=255) == 1 and attend(L, c, stride=260) == 1
