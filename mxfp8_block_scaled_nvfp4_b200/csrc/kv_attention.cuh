@@ -125,6 +125,7 @@ struct Geo {
   static constexpr int kbytes = DP / 4 * (int)Fmt<MODE>::bits / 8, kw = kbytes / 4;  // a lane's share of a key row
   static constexpr int vbytes = DP / 8 * (int)Fmt<MODE>::bits / 8, vw = vbytes / 4;  // and of a value row
   static constexpr int ksteps = DP / 16, mtiles = DP / 16;
+  static constexpr int krow = DP * (int)Fmt<MODE>::bits / 8, srow = DP / (int)Fmt<MODE>::group;  // a row's bytes
   static constexpr int ts = (MODE == kMX8 || DP == 256) ? 1 : 2;  // 16-token tiles a step: what 255 registers hold
 };
 
@@ -215,6 +216,14 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// N scale bytes (N < 1: the byte that several lanes share).
+template <int N>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
+  if constexpr (N <= 1) return __ldg(p);
+  else if constexpr (N == 2) return __ldg(reinterpret_cast<const uint16_t*>(p));
+  else return __ldg(reinterpret_cast<const uint32_t*>(p));
+}
+
 // A lane's key words and scales of one token row; `row` < 0 gives zeros.
 // 32 elements (one piece) is what D is a multiple of.
 template <int MODE, int DP>
@@ -267,7 +276,10 @@ __device__ __forceinline__ void load_value(const AttnArgs& a, int64_t row, uint3
     sc = __ldg(s + g * per / group);
 }
 
-template <typename QT, int MODE, int DP, int NT, bool P16>
+// FAST: D == DP, 16-token tiles lie on one page and rows have 32-bit numbers;
+// a step wholly inside the range then loads without a check at fixed offsets
+// from one row.  Everything else looks each row up.
+template <typename QT, int MODE, int DP, int NT, bool FAST>
 struct Decode {
   using G = Geo<MODE, DP>;
   static constexpr int TS = G::ts;
@@ -347,51 +359,59 @@ struct Decode {
     }
     return (int64_t)(((uint64_t)page * a.heads + hk) * a.page_size + ((uint32_t)j - pg * a.page_size));
   }
-  // Row of token j0 of a 16-token tile that lies on one page (P16), whatever
-  // of the tile is inside the range; -1 where none is or the page is not one.
-  __device__ __forceinline__ int64_t tile_row(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j0, const Range& rg) const {
-    if (j0 + 16 <= rg.lo || j0 >= rg.hi) return -1;
-    const uint32_t pg = a.by_page.div((uint32_t)j0);
-    const int32_t page = __ldg(table + pg);
-    if (page < 0 || (uint32_t)page >= a.num_pages) {
-      atomicOr(&g_device_error, (unsigned)kDevErrIndex);
-      return -1;
-    }
-    return (int64_t)(((uint64_t)page * a.heads + hk) * a.page_size + ((uint32_t)j0 - pg * a.page_size));
+  // FAST: row of token 0 of a 16-token tile on page `page`.
+  __device__ __forceinline__ uint32_t tile_row(const AttnArgs& a, int32_t page, uint32_t hk, int32_t j0) const {
+    return ((uint32_t)page * a.heads + hk) * a.page_size + ((uint32_t)j0 - a.by_page.div((uint32_t)j0) * a.page_size);
   }
 
   // Bit 2t + i of the result: token 16 t + 8 i + g of the step is there.
   __device__ __forceinline__ uint32_t load_keys(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j0, const Range& rg,
-                                                const int64_t (&rows)[TS]) {
+                                                bool inside, const uint32_t (&rows)[TS]) {
+    if (FAST && inside) {
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        const uint8_t* p = a.codes[0] + (uint64_t)(rows[t] + g) * G::krow + c * G::kbytes;
+        const uint8_t* q = a.scales[0] + (uint64_t)(rows[t] + g) * G::srow + c * (DP / 4) / Fmt<MODE>::group;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          load_words<G::kbytes>(p + 8 * i * G::krow, kw[t][i]);
+          ks[t][i] = load_scales<DP / 4 / Fmt<MODE>::group>(q + 8 * i * G::srow);
+        }
+      }
+      return (1u << (2 * TS)) - 1u;
+    }
     uint32_t there = 0;
 #pragma unroll
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int32_t j = j0 + 16 * t + 8 * i + g;
-        int64_t row;
-        if constexpr (P16)
-          row = rows[t] >= 0 && j >= rg.lo && j < rg.hi ? rows[t] + 8 * i + g : -1;
-        else
-          row = row_at(a, table, hk, j, rg);
+        const int64_t row = row_at(a, table, hk, j0 + 16 * t + 8 * i + g, rg);
         there |= (row >= 0 ? 1u : 0u) << (2 * t + i);
         load_key<MODE, DP>(a, row, c, kw[t][i], ks[t][i]);
       }
     return there;
   }
   __device__ __forceinline__ void load_values(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j0, const Range& rg,
-                                              const int64_t (&rows)[TS]) {
+                                              bool inside, const uint32_t (&rows)[TS]) {
+    if (FAST && inside) {
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        const uint8_t* p = a.codes[1] + (uint64_t)(rows[t] + 2 * c) * G::krow + g * G::vbytes;
+        const uint8_t* q = a.scales[1] + (uint64_t)(rows[t] + 2 * c) * G::srow + g * (DP / 8) / Fmt<MODE>::group;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = (i & 1) + 8 * (i >> 1);
+          load_words<G::vbytes>(p + x * G::krow, vw[t][i]);
+          vs[t][i] = load_scales<DP / 8 / Fmt<MODE>::group>(q + x * G::srow);
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int t = 0; t < TS; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t x = 2 * c + (i & 1) + 8 * (i >> 1);
-        const int32_t j = j0 + 16 * t + x;
-        int64_t row;
-        if constexpr (P16)
-          row = rows[t] >= 0 && j >= rg.lo && j < rg.hi ? rows[t] + x : -1;
-        else
-          row = row_at(a, table, hk, j, rg);
+        const int64_t row = row_at(a, table, hk, j0 + 16 * t + 2 * c + (i & 1) + 8 * (i >> 1), rg);
         load_value<MODE, DP>(a, row, g, vw[t][i], vs[t][i]);
       }
   }
@@ -520,9 +540,9 @@ struct Decode {
   }
 };
 
-template <typename QT, int MODE, int DP, int NT, bool P16>
+template <typename QT, int MODE, int DP, int NT, bool FAST>
 __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant__ AttnArgs a) {
-  using D = Decode<QT, MODE, DP, NT, P16>;
+  using D = Decode<QT, MODE, DP, NT, FAST>;
   constexpr int TS = D::TS, MT = D::G::mtiles, STEP = 16 * TS, ROWS = 8 * NT;
   __shared__ float sm[kDecWarps][ROWS], sl[kDecWarps][ROWS];
   __shared__ float so[kDecWarps / 2][ROWS * DP];
@@ -569,17 +589,32 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   if (a.window) all_lo = tile_range(a, s, i1, i1).lo;
   if (a.causal) all_hi = min(end, tile_range(a, s, i0, i0).hi);
 
-  int64_t rows[TS];
+  // The loads of the next step are issued as soon as this one's registers are
+  // free: keys after the logits, values after the weighted sum; the page
+  // numbers a step earlier still.
   int32_t j0 = begin + (int32_t)warp * STEP;
-  auto find = [&](int32_t j) {
+  int32_t pages[TS];
+  auto look = [&](int32_t j) {
 #pragma unroll
-    for (int t = 0; t < TS; ++t) rows[t] = P16 ? d.tile_row(a, table, hk, j + 16 * t, here) : 0;
+    for (int t = 0; t < TS; ++t) pages[t] = FAST && j + 16 * t < end ? __ldg(table + a.by_page.div((uint32_t)(j + 16 * t))) : -1;
+  };
+  uint32_t rows[TS];
+  bool inside = false;
+  auto find = [&](int32_t j) {
+    inside = FAST && j >= rg.lo && j + STEP <= end;
+#pragma unroll
+    for (int t = 0; t < TS; ++t) {
+      inside = inside && (uint32_t)pages[t] < a.num_pages;
+      rows[t] = d.tile_row(a, pages[t], hk, j + 16 * t);
+    }
   };
   uint32_t there = 0;
   if (j0 < end) {
+    look(j0);
     find(j0);
-    there = d.load_keys(a, table, hk, j0, here, rows);
-    d.load_values(a, table, hk, j0, here, rows);
+    look(j0 + kDecWarps * STEP);
+    there = d.load_keys(a, table, hk, j0, here, inside, rows);
+    d.load_values(a, table, hk, j0, here, inside, rows);
   }
   for (; j0 < end; j0 += kDecWarps * STEP) {
     const int32_t jn = j0 + kDecWarps * STEP;
@@ -589,7 +624,8 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
     for (int t = 0; t < TS; ++t) d.logits(t, sv[t]);
     if (jn < end) {
       find(jn);
-      there = d.load_keys(a, table, hk, jn, here, rows);
+      look(jn + kDecWarps * STEP);
+      there = d.load_keys(a, table, hk, jn, here, inside, rows);
     }
     const bool full = __all_sync(0xffffffffu, now == (1u << (2 * TS)) - 1u) && j0 >= all_lo && j0 + STEP <= all_hi;
     if (!full) {
@@ -636,6 +672,11 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
           }
         }
     }
+    float ref[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[nt][e] = d.m[nt][e] == -INFINITY ? 0.0f : d.m[nt][e];
 #pragma unroll
     for (int t = 0; t < TS; ++t) {
       uint32_t ph[NT][2], pl[NT][2];
@@ -644,8 +685,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float ref = d.m[nt][e & 1] == -INFINITY ? 0.0f : d.m[nt][e & 1];
-          p[e] = ex2(fmaf(sv[t][nt][e], d.fz[nt][e & 1], -ref));
+          p[e] = ex2(fmaf(sv[t][nt][e], d.fz[nt][e & 1], -ref[nt][e & 1]));
           d.l[nt][e & 1] += p[e];
         }
 #pragma unroll
@@ -662,7 +702,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
       }
       d.weigh(t, ph, pl);
     }
-    if (jn < end) d.load_values(a, table, hk, jn, here, rows);
+    if (jn < end) d.load_values(a, table, hk, jn, here, inside, rows);
   }
 
   // Join the warps: a common maximum first, then the sums, two warps at a time.

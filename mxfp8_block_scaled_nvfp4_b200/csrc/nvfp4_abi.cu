@@ -1036,7 +1036,7 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   const int64_t tiles = (max_q * a.G + p.tile_rows - 1) / p.tile_rows;
   if (product_exceeds(tiles, p.chunks, INT32_MAX)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q and max_kv too large", tag);
   const dim3 grid((unsigned)(tiles * p.chunks), a.heads, a.B);
-  const bool p16 = a.page_size % 16 == 0;
+  const bool one_page = a.page_size % 16 == 0 && !product_exceeds(cache->num_pages * cache->page_size, cache->heads, UINT32_MAX);
   dispatch_mode(cache->mode, [&](auto m) {
     constexpr int MODE = decltype(m)::value;
     auto with_type = [&](auto t) {
@@ -1044,13 +1044,14 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
       auto with_dim = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
         auto go = [&](auto kern) { kern<<<grid, kv::kDecThreads, 0, stream>>>(a); };
+        const bool fast = one_page && a.D == (uint32_t)DP;
         if constexpr (DP <= 128) {
           if (p.tile_rows == 16) {
-            p16 ? go(kv::k_kv_decode<QT, MODE, DP, 2, true>) : go(kv::k_kv_decode<QT, MODE, DP, 2, false>);
+            fast ? go(kv::k_kv_decode<QT, MODE, DP, 2, true>) : go(kv::k_kv_decode<QT, MODE, DP, 2, false>);
             return;
           }
         }
-        p16 ? go(kv::k_kv_decode<QT, MODE, DP, 1, true>) : go(kv::k_kv_decode<QT, MODE, DP, 1, false>);
+        fast ? go(kv::k_kv_decode<QT, MODE, DP, 1, true>) : go(kv::k_kv_decode<QT, MODE, DP, 1, false>);
       };
       if (a.D <= 64) with_dim(std::integral_constant<int, 64>{});
       else if (a.D <= 128) with_dim(std::integral_constant<int, 128>{});
