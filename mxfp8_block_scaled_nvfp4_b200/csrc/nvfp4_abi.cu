@@ -20,6 +20,7 @@
 #include "gather_qmm.cuh"
 #include "kv_cache.cuh"
 #include "kv_attention.cuh"
+#include "kv_prefill.cuh"
 
 using namespace nvfp4;
 
@@ -921,28 +922,31 @@ nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
   return check_launch(tag);
 }
 
-// How kv_attention cuts its work: rows of queries a CTA holds, tokens a CTA
-// walks and the largest number of such chunks a row tile can have.
+// How kv_attention cuts its work: the kernel, rows of queries a CTA holds,
+// tokens a CTA walks and the largest number of such chunks a row tile can have.
 struct KvPlan {
+  bool prefill;
   int64_t tile_rows, chunk, chunks, bytes_per_chunk;
 };
 static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
-                      int64_t window, size_t workspace_bytes) {
+                      int64_t window, bool prefill_has_it, size_t workspace_bytes) {
   KvPlan p;
   const int64_t rows = max_q * (Hq / heads);
-  p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;
+  p.prefill = prefill_has_it && rows > 32;
+  p.tile_rows = p.prefill ? (D > 128 ? 128 : 256) : rows <= 8 || D > 128 ? 8 : 16;
   p.bytes_per_chunk = T * Hq * (D * 4 + 8);
   // tokens a tile's range can span, from a multiple of 16
   int64_t span = max_kv;
   if (window > 0 && window + max_q + 30 < span) span = window + max_q + 30;
   const double tiles = (double)B * (double)heads * (double)((rows + p.tile_rows - 1) / p.tile_rows);
-  const double share = (double)span * tiles / (148 * 6);  // may exceed 64-bit integers
+  const int64_t least = p.prefill ? 512 : 128;
+  const double share = (double)span * tiles / (p.prefill ? 148 : 148 * 6);  // may exceed 64-bit integers
   int64_t chunk = share < (double)span ? (int64_t)share + 1 : span;
   int64_t fit = workspace_bytes == SIZE_MAX ? span : (int64_t)(workspace_bytes / (size_t)p.bytes_per_chunk);
   if (fit < 2) fit = 1;
   if ((span + fit - 1) / fit > chunk) chunk = (span + fit - 1) / fit;
   p.chunk = (chunk + 127) / 128 * 128;
-  if (p.chunk < 128) p.chunk = 128;
+  if (p.chunk < least) p.chunk = least;
   p.chunks = span > 0 ? (span + p.chunk - 1) / p.chunk : 1;
   return p;
 }
@@ -953,8 +957,13 @@ size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t hea
       Hq % heads != 0 || D < 32 || D > 256 || D % 32 != 0 || max_q < 1 || max_q > (1 << 30) || max_kv < 0 ||
       max_kv > (1 << 30) || window < 0 || product_exceeds(T, Hq * D, kMaxElems))
     return 0;
-  const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, SIZE_MAX);
-  return p.chunks > 1 ? (size_t)(p.chunks * p.bytes_per_chunk) : 0;
+  size_t most = 0;  // over the kernels that the types may choose
+  for (int i = 0; i < 2; ++i) {
+    const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, SIZE_MAX);
+    const size_t bytes = p.chunks > 1 ? (size_t)(p.chunks * p.bytes_per_chunk) : 0;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
@@ -1027,7 +1036,8 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.window = window > (1 << 30) ? 0u : (uint32_t)window;  // a window past any length hides nothing
   a.causal = causal != 0;
   a.by_page.init(a.page_size);
-  const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, workspace_bytes);
+  const bool prefill_has_it = cache->mode == NVFP4_MODE_NVFP4 || q_dt == NVFP4_DT_BF16;
+  const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, prefill_has_it, workspace_bytes);
   a.chunk = (int32_t)p.chunk;
   a.chunks = (uint32_t)p.chunks;
   a.tile_rows = (uint32_t)p.tile_rows;
@@ -1037,12 +1047,21 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   if (product_exceeds(tiles, p.chunks, INT32_MAX)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q and max_kv too large", tag);
   const dim3 grid((unsigned)(tiles * p.chunks), a.heads, a.B);
   const bool one_page = a.page_size % 16 == 0 && !product_exceeds(cache->num_pages * cache->page_size, cache->heads, UINT32_MAX);
+  cudaError_t e = cudaSuccess;
   dispatch_mode(cache->mode, [&](auto m) {
     constexpr int MODE = decltype(m)::value;
     auto with_type = [&](auto t) {
       using QT = decltype(t);
       auto with_dim = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
+        if (p.prefill) {
+          if constexpr (MODE == kv::kNV || std::is_same<QT, __nv_bfloat16>::value) {
+            auto kern = kv::pf::k_kv_prefill<QT, MODE, DP>;
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv::pf::Shape<DP>::smem);
+            if (e == cudaSuccess) kern<<<grid, kv::pf::THREADS, kv::pf::Shape<DP>::smem, stream>>>(a);
+          }
+          return;
+        }
         auto go = [&](auto kern) { kern<<<grid, kv::kDecThreads, 0, stream>>>(a); };
         const bool fast = one_page && a.D == (uint32_t)DP;
         if constexpr (DP <= 128) {
@@ -1056,11 +1075,12 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
       if (a.D <= 64) with_dim(std::integral_constant<int, 64>{});
       else if (a.D <= 128) with_dim(std::integral_constant<int, 128>{});
       else with_dim(std::integral_constant<int, 256>{});
-      if (p.chunks > 1) kv::k_kv_join<QT><<<dim3(a.max_q, a.Hq, a.B), kv::kJoinWarps * 32, 0, stream>>>(a);
+      if (e == cudaSuccess && p.chunks > 1) kv::k_kv_join<QT><<<dim3(a.max_q, a.Hq, a.B), kv::kJoinWarps * 32, 0, stream>>>(a);
     };
     if (q_dt == NVFP4_DT_F16) with_type(__half{});
     else with_type(__nv_bfloat16{});
   });
+  if (e != cudaSuccess) return fail(NVFP4_ERR_CUDA, "[%s] %s", tag, cudaGetErrorString(e));
   return check_launch(tag);
 }
 
