@@ -35,6 +35,7 @@ using namespace tc;
 
 constexpr int W_PROD = 8, W_MMA = 12, THREADS = 13 * 32, PROD = 128;
 constexpr int ST = 2;  // K and V stages
+constexpr int kPolyEvery = 4;  // of so many pairs of exponentials one is a polynomial on the FMA pipes
 
 template <int DP>
 struct Shape {
@@ -102,25 +103,31 @@ __device__ __forceinline__ uint4 decode8(const uint32_t* w, uint32_t f) {
 }
 
 // One thread's share of a K or V tile: units of 32 elements of one token
-// (DP / 32 units a token, U a thread, in registers from load to store).
+// (DP / 32 units a token, U a thread, in registers from load to store).  Unit
+// u is the same part c of token tok + u * PROD / (DP / 32).
 template <int MODE, int DP>
 struct Share {
   static constexpr int per_row = DP / 32, U = Shape<DP>::NT * per_row / PROD;
-  static constexpr int words = 4 * (int)Fmt<MODE>::bits / 4;  // of a unit
+  static constexpr int words = (int)Fmt<MODE>::bits, wo = words / 4;  // of a unit, of an octet
+  static constexpr uint32_t step = PROD / per_row;                    // tokens between units (a multiple of 8)
   uint32_t w[U][words], s[U];
 
-  __device__ __forceinline__ void load(const AttnArgs& a, int side, const int64_t* rows, uint32_t p) {
+  // at: byte offsets of the tokens' code rows and scale rows, < 0 for tokens
+  // that are not there: those get another row's codes with a scale of zero
+  // (finite numbers that P = 0 meets).
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const int64_t (*at)[2], uint32_t tok,
+                                       uint32_t c, uint32_t D) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t x = p + (uint32_t)u * PROD, tok = x / per_row, c = x % per_row;
-      const int64_t row = rows[tok];
+      const int64_t x = at[tok + u * step][0], y = at[tok + u * step][1];
+      if (c * 32u < D) {  // the same for all units of a thread
+        load_words<4 * words>(codes + (x < 0 ? 0 : x) + c * (4 * words), w[u]);
+        s[u] = load_scales<32 / (int)Fmt<MODE>::group>(scales + (x < 0 ? 0 : y) + c * (32 / Fmt<MODE>::group));
+        if (x < 0) s[u] = 0;
+      } else {
 #pragma unroll
-      for (int i = 0; i < words; ++i) w[u][i] = 0;
-      s[u] = 0;
-      if (row >= 0 && c * 32u < a.D) {
-        load_words<4 * words>(a.codes[side] + (uint64_t)row * (a.D * Fmt<MODE>::bits / 8u) + c * (4 * words), w[u]);
-        s[u] = load_scales<32 / (int)Fmt<MODE>::group>(a.scales[side] + (uint64_t)row * (a.D / Fmt<MODE>::group) +
-                                                        c * (32 / Fmt<MODE>::group));
+        for (int i = 0; i < words; ++i) w[u][i] = 0;
+        s[u] = 0;
       }
     }
   }
@@ -128,34 +135,101 @@ struct Share {
   // of a row lie in another box at the same banks as units 0, 1: they store
   // their octets in another order, so that eight lanes (two rows) always
   // cover eight chunks.
-  __device__ __forceinline__ void store(uint32_t base, uint32_t p) const {
+  __device__ __forceinline__ void store(uint32_t base, uint32_t tok, uint32_t c) const {
+    const bool swap = per_row >= 4 && (c & 2u);
+    const uint32_t row = base + (tok >> 3) * Shape<DP>::group + (c >> 1) * 1024u + (tok & 7u) * 128u;
+    uint32_t to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      to[e] = row + ((((c & 1u) * 4u + (uint32_t)(swap ? e ^ 2 : e)) ^ (tok & 7u)) << 4);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t x = p + (uint32_t)u * PROD, tok = x / per_row, c = x % per_row;
-      const uint32_t at = base + (tok >> 3) * Shape<DP>::group + (c >> 1) * 1024u + (tok & 7u) * 128u;
       uint32_t f[2];
       if constexpr (MODE == kNV) {
         const uint32_t pr = e4m3x2_to_f16x2(s[u]);
-        f[0] = __byte_perm(pr, 0, 0x1010);
-        f[1] = __byte_perm(pr, 0, 0x3232);
+        f[0] = __byte_perm(pr, 0, swap ? 0x3232 : 0x1010);
+        f[1] = __byte_perm(pr, 0, swap ? 0x1010 : 0x3232);
       } else {
         const uint32_t q = mx_factor<MODE>(s[u]);
         f[0] = f[1] = q | (q << 16);
       }
-      constexpr int wo = words / 4;  // words an octet
-      uint4 v[4];
+      uint32_t x[words];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = decode8<MODE>(&w[u][e * wo], f[e / 2]);
-      const bool swap = per_row >= 4 && (c & 2u);
+      for (int i = 0; i < words; ++i) x[i] = swap ? w[u][i ^ (2 * wo)] : w[u][i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint4 y = swap ? v[e ^ 2] : v[e];
-        const uint32_t oct = (uint32_t)(swap ? e ^ 2 : e);
-        st_shared_v4(at + ((((c & 1u) * 4u + oct) ^ (tok & 7u)) << 4), y);
-      }
+      for (int e = 0; e < 4; ++e) st_shared_v4(to[e] + u * (step / 8u) * Shape<DP>::group, decode8<MODE>(&x[e * wo], f[e / 2]));
     }
   }
 };
+
+// tcgen05.ld of 32 columns without its wait; the wait names the registers, so
+// that nothing reads them before it.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Packed pairs of fp32.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^y of a pair on the FMA pipes: y = n + f with n the nearest integer (from
+// the low bits of y + 1.5 * 2^23), 2^f by the degree-4 polynomial of least
+// relative error on [-1/2, 1/2] (Remez exchange; 2.6e-6, a hundredth of P's
+// rounding), n added to the exponent.  y is raised to -126 first, so nothing
+// wraps; what is masked becomes 2^-126.
+__device__ __forceinline__ uint64_t ex2_poly(uint64_t y2) {
+  float y0, y1;
+  unpair(y2, y0, y1);
+  y2 = pair(fmaxf(y0, -126.0f), fmaxf(y1, -126.0f));
+  const uint64_t big = pair(12582912.0f, 12582912.0f), t = add2(y2, big);
+  const uint64_t f = fma2(add2(t, pair(-12582912.0f, -12582912.0f)), pair(-1.0f, -1.0f), y2);
+  uint64_t p = fma2(f, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
+  float t0, t1, p0, p1;
+  unpair(t, t0, t1);
+  unpair(p, p0, p1);
+  return pair(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
+              __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
+}
 
 template <typename QT, int MODE, int DP>
 __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant__ AttnArgs a) {
@@ -164,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   constexpr bool kMx = MODE != kNV;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], o_done[2], all_done;
-  __shared__ int64_t rows[2][NT];
+  __shared__ int64_t rows[2][NT][2];  // byte offsets of the tokens' code and scale rows
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_flag;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -270,7 +344,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
           if ((uint32_t)page < a.num_pages)
             x = (int64_t)(((uint64_t)page * a.heads + hk) * a.page_size + ((uint32_t)j - pg * a.page_size));
         }
-        rows[n & 1][p] = x;
+        rows[n & 1][p][0] = x * (int64_t)(a.D * Fmt<MODE>::bits / 8u);
+        rows[n & 1][p][1] = x * (int64_t)(a.D / Fmt<MODE>::group);
       }
       uint32_t stop;
       asm volatile(
@@ -281,27 +356,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
           : "memory");
       return stop != 0;
     };
-    Share<MODE, DP> kk, vv;
+    using Sh = Share<MODE, DP>;
+    Sh kk, vv;
+    const uint32_t tok = p / Sh::per_row, c = p % Sh::per_row;
     look(0);
     if (iters > 0) {
-      kk.load(a, 0, rows[0], p);
-      vv.load(a, 1, rows[0], p);
+      kk.load(a.codes[0], a.scales[0], rows[0], tok, c, a.D);
+      vv.load(a.codes[1], a.scales[1], rows[0], tok, c, a.D);
     }
     look(1);
     for (int32_t n = 0; n < iters; ++n) {
       const uint32_t st = (uint32_t)n % ST, ph = ((uint32_t)n / ST) & 1u;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&k_empty[st]), ph ^ 1u)) || abort_flag) abort_flag = 1;
-      kk.store(sk + st * S::kv_tile, p);
+      kk.store(sk + st * S::kv_tile, tok, c);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&k_full[st]));
-      if (n + 1 < iters) kk.load(a, 0, rows[(n + 1) & 1], p);
+      if (n + 1 < iters) kk.load(a.codes[0], a.scales[0], rows[(n + 1) & 1], tok, c, a.D);
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&v_empty[st]), ph ^ 1u)) || abort_flag) abort_flag = 1;
-      vv.store(sv + st * S::kv_tile, p);
+      vv.store(sv + st * S::kv_tile, tok, c);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(smem_u32(&v_full[st]));
-      if (n + 1 < iters) vv.load(a, 1, rows[(n + 1) & 1], p);
+      if (n + 1 < iters) vv.load(a.codes[1], a.scales[1], rows[(n + 1) & 1], tok, c, a.D);
       if (look(n + 2)) break;  // rows[n & 1]: every thread read it for tile n before the last look
     }
   } else if (warp == W_MMA) {
@@ -384,24 +461,44 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       }
       tc_fence_after();
       const bool masked = any_bad || j0 < all_lo || j0 + NT > all_hi;
-      auto mask = [&](int c, float (&x)[32]) {  // columns 32c .. of this row
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int32_t j = j0 + 32 * c + e;
-          bool in = j >= see.lo && j < see.hi && j < end;
-          if (any_bad && in) in = (uint32_t)__ldg(table + a.by_page.div((uint32_t)j)) < a.num_pages;
-          if (!in) x[e] = -INFINITY;
-        }
-      };
-      float top = -INFINITY;
+      constexpr int NC = NT / 32;
+      uint32_t x[2][32];
+      if (masked) {  // minus infinity into S itself; few tiles have a border
 #pragma unroll 1
-      for (int c = 0; c < NT / 32; ++c) {
-        float x[32];
-        tmem_ld32(ts_ + 32u * c, x);
-        if (masked) mask(c, x);
+        for (int c = 0; c < NC; ++c) {
+          tmem_ld32_start(ts_ + 32u * c, x[0]);
+          tmem_ld32_wait(x[0]);
+          const int32_t jc = j0 + 32 * c;
+          const int32_t lo = see.lo - jc, hi = min(see.hi, end) - jc;
+          uint32_t in = (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u) & (hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u);
+          if (any_bad)
+            for (int e = 0; e < 32; ++e)
+              if (((in >> e) & 1u) && (uint32_t)__ldg(table + a.by_page.div((uint32_t)(jc + e))) >= a.num_pages) in &= ~(1u << e);
+          uint32_t y[2][16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+          for (int e = 0; e < 32; ++e) y[e / 16][e % 16] = (in >> e) & 1u ? x[0][e] : 0xFF800000u;
+          tmem_st<16>(ts_ + 32u * c, y[0]);
+          tmem_st<16>(ts_ + 32u * c + 16u, y[1]);
+        }
+        tmem_wait_st();
       }
+      float top;
+      tmem_ld32_start(ts_, x[0]);
+      {
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          tmem_ld32_wait(x[c & 1]);
+          if (c + 1 < NC) tmem_ld32_start(ts_ + 32u * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              t4[k] = max3(t4[k], __uint_as_float(x[c & 1][e + 2 * k]), __uint_as_float(x[c & 1][e + 2 * k + 1]));
+        }
+        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      }
+      tmem_ld32_start(ts_, x[0]);
       top = top * fz - (kMx ? 32.0f : 0.0f);
       // the reference moves only when exceeded by 2^8 (see k_kv_decode)
       if (__any_sync(0xffffffffu, top > m + 8.0f)) {
@@ -415,12 +512,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
             break;
           }
           tc_fence_after();
+          tmem_ld32_wait(x[0]);  // the load above ends before x[1] waits for others
           for (uint32_t c = 0; c < a.D; c += 32u) {
-            float x[32];
-            tmem_ld32(to + c, x);
+            tmem_ld32_start(to + c, x[1]);
+            tmem_ld32_wait(x[1]);
             uint32_t y[2][16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e / 16][e % 16] = __float_as_uint(x[e] * f);
+            for (int e = 0; e < 32; ++e) y[e / 16][e % 16] = __float_as_uint(__uint_as_float(x[1][e]) * f);
             tmem_st<16>(to + c, y[0]);
             tmem_st<16>(to + c + 16u, y[1]);
           }
@@ -428,16 +526,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-      for (int c = 0; c < NT / 32; ++c) {
-        float x[32];
-        tmem_ld32(ts_ + 32u * c, x);
-        if (masked) mask(c, x);
+      const uint64_t fz2 = pair(fz, fz), ref2 = pair(-ref, -ref);
+      uint64_t l2[2] = {0, 0};
+      auto weights = [&](int c, const uint32_t (&z)[32]) {
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2(fmaf(x[2 * e], fz, -ref)), p1 = ex2(fmaf(x[2 * e + 1], fz, -ref));
-          l += p0 + p1;
+          uint64_t y = fma2(pair(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), fz2, ref2);
+          float p0, p1;
+          if (e % kPolyEvery == kPolyEvery - 1) {
+            y = ex2_poly(y);
+            unpair(y, p0, p1);
+          } else {
+            unpair(y, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            y = pair(p0, p1);
+          }
+          l2[e & 1] = add2(l2[e & 1], y);
           if constexpr (!kMx) {
             hi[e] = pack_f16x2(p0, p1);
           } else {
@@ -451,6 +557,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
           tmem_st<16>(ts_ + 32u * c, hi);
           tmem_st<16>(ts_ + 32u * c + 16u, lo);
         }
+      };
+#pragma unroll 1  // twice NC / 2: the loop body stays in the instruction cache
+      for (int c = 0; c < NC; c += 2) {
+        tmem_ld32_wait(x[0]);
+        tmem_ld32_start(ts_ + 32u * (c + 1), x[1]);
+        weights(c, x[0]);
+        tmem_ld32_wait(x[1]);
+        if (c + 2 < NC) tmem_ld32_start(ts_ + 32u * (c + 2), x[0]);
+        weights(c + 1, x[1]);
+      }
+      {
+        float s0, s1;
+        unpair(add2(l2[0], l2[1]), s0, s1);
+        l += s0 + s1;
       }
       tmem_wait_st();
       tc_fence_before();
@@ -467,6 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       const uint32_t h = hk * a.G + (min(r, R - 1u) - i * a.G);
       const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
       const float fv = kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
+      if (m == -INFINITY) l = 0.0f;  // nothing seen (ex2_poly leaves 2^-126)
       const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
       if (r < R) {
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);

@@ -1036,7 +1036,9 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.window = window > (1 << 30) ? 0u : (uint32_t)window;  // a window past any length hides nothing
   a.causal = causal != 0;
   a.by_page.init(a.page_size);
-  const bool prefill_has_it = cache->mode == NVFP4_MODE_NVFP4 || q_dt == NVFP4_DT_BF16;
+  // k_kv_prefill: no two-term Q for fp16 over the MX modes; it loads some row
+  // for every token, so there has to be one
+  const bool prefill_has_it = (cache->mode == NVFP4_MODE_NVFP4 || q_dt == NVFP4_DT_BF16) && cache->num_pages > 0;
   const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, prefill_has_it, workspace_bytes);
   a.chunk = (int32_t)p.chunk;
   a.chunks = (uint32_t)p.chunks;
