@@ -34,6 +34,7 @@ struct AttnArgs {
   int32_t chunk;                // tokens a CTA walks (a multiple of 16, at most 2^30)
   uint32_t chunks;              // CTAs a row tile has
   uint32_t tile_rows;           // query rows a CTA holds
+  uint64_t scale_bytes;         // of one side
   float2* part_ml;              // [chunks, T, Hq]
   float* part_o;                // [chunks, T, Hq, D]
   FastDiv by_page;

@@ -4,10 +4,16 @@
 // A CTA holds one or two tiles of 128 query rows (row r of a sequence and a
 // key/value head is query r / G, head r % G of the group) and walks the
 // tokens in tiles of NT:
-//   warps 0-3, 4-7  softmax of query tile 0, 1; thread = row = TMEM lane
-//   warps 8-11      producers: cache codes to 16-bit K_hat and V_hat tiles in
-//                   shared memory (each decoded once for both query tiles)
-//   warp 12         allocates TMEM and issues the MMAs
+//   warps 0-7       producers: cache codes to 16-bit K_hat and V_hat tiles in
+//                   shared memory (each decoded once for both query tiles).  A
+//                   thread owns a part of a token: it copies its codes and scales
+//                   (cp.async) into its own slots a tile ahead and decodes them
+//                   from there, so the threads need no barrier; K and V run
+//                   through the same loop body, which keeps it small (with the
+//                   bodies unrolled the producers waited for instructions)
+//   warp 8          allocates TMEM and issues the MMAs
+//   warps 12-19, 20-27 softmax of query tile 0, 1; a row (TMEM lane) has two
+//                   threads, one for each half of the tile's tokens
 // Per query tile, S = Q K_hat^T (128 x NT, fp32, TMEM); the softmax threads
 // write P as 16-bit pairs over S, and O (128 x D, fp32, TMEM) += P V_hat with
 // P as the MMA's TMEM operand.  The two query tiles alternate, so that the
@@ -33,22 +39,69 @@ namespace pf {
 
 using namespace tc;
 
-constexpr int W_PROD = 8, W_MMA = 12, THREADS = 13 * 32, PROD = 128;
-constexpr int ST = 2;  // K and V stages
-constexpr int kPolyEvery = 4;  // of so many pairs of exponentials one is a polynomial on the FMA pipes
+constexpr int W_MMA = 8, W_SOFT = 12, THREADS = 28 * 32, PROD = 256;
 
-template <int DP>
+template <int MODE, int DP>
 struct Shape {
   static constexpr int NQ = DP == 256 ? 1 : 2;        // query tiles a CTA
   static constexpr int NT = DP == 256 ? 64 : 128;     // tokens a tile
+  static constexpr int HC = NT / 2;                   // tokens of a softmax thread
   static constexpr uint32_t group = DP / 64 * 1024;   // an 8-row group
   static constexpr uint32_t q_tile = 16 * group;      // 128 rows
   static constexpr uint32_t kv_tile = NT / 8 * group;
+  // tiles in shared memory: two of K and V, but one of V where MXFP8's raw codes take the room
+  static constexpr uint32_t st_k = 2, st_v = MODE == kMX8 && DP >= 128 ? 1 : 2;
+  static constexpr int EPT = DP * NT / PROD;          // elements of a producer thread: 32 or 64
+  static constexpr uint32_t raw_codes = PROD * EPT * Fmt<MODE>::bits / 8u, raw = raw_codes + 8u * PROD;
+  static constexpr uint32_t at_k = NQ * q_tile, at_v = at_k + st_k * kv_tile, at_raw = at_v + st_v * kv_tile;
   // at least half an SM's: a CTA takes all of TMEM, so one fits at a time
-  static constexpr uint32_t bytes = NQ * q_tile + 2 * ST * kv_tile + 1024, smem = bytes < 122880 ? 122880 : bytes;
+  static constexpr uint32_t bytes = at_raw + 2 * raw + 1024, smem = bytes < 122880 ? 122880 : bytes;
   static constexpr uint32_t tm_s = 0, tm_o = 256;     // TMEM columns: S of tile t at 128 t, O at 256 + 128 t
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t at) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// tc::mbar_wait with a hint of how long (in ns) the thread may be suspended: a
+// warp that polls takes issue slots from the ones it waits for.  At most
+// 2^17 * 20 us.
+__device__ __forceinline__ bool wait_for(uint64_t& bar, uint32_t parity) {
+  for (uint32_t i = 0; i < (1u << 17); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(&bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+  }
+  atomicOr(&g_device_error, (unsigned)kDevErrTimeout);
+  return false;
+}
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -102,62 +155,66 @@ __device__ __forceinline__ uint4 decode8(const uint32_t* w, uint32_t f) {
   }
 }
 
-// One thread's share of a K or V tile: units of 32 elements of one token
-// (DP / 32 units a token, U a thread, in registers from load to store).  Unit
-// u is the same part c of token tok + u * PROD / (DP / 32).
+// A producer thread's slots of one side: its codes, 16-byte piece k at
+// [k][thread], and the one or two aligned 32-bit words that hold its scales
+// (two where a row's scale bytes are no multiple of four).
 template <int MODE, int DP>
-struct Share {
-  static constexpr int per_row = DP / 32, U = Shape<DP>::NT * per_row / PROD;
-  static constexpr int words = (int)Fmt<MODE>::bits, wo = words / 4;  // of a unit, of an octet
-  static constexpr uint32_t step = PROD / per_row;                    // tokens between units (a multiple of 8)
-  uint32_t w[U][words], s[U];
-
-  // at: byte offsets of the tokens' code rows and scale rows, < 0 for tokens
-  // that are not there: those get another row's codes with a scale of zero
-  // (finite numbers that P = 0 meets).
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const int64_t (*at)[2], uint32_t tok,
-                                       uint32_t c, uint32_t D) {
+struct Raw {
+  using S = Shape<MODE, DP>;
+  static constexpr int pieces = S::EPT * (int)Fmt<MODE>::bits / 128, units = S::EPT / 32;
+  static constexpr uint32_t nb = S::EPT / Fmt<MODE>::group;  // scale bytes
+  // Starts the copies of cache row `row`, elements e0 .. e0 + EPT; returns the
+  // scales' offset in their first word.
+  static __device__ __forceinline__ uint32_t fetch(const AttnArgs& a, const uint8_t* codes, const uint8_t* scales, uint64_t row,
+                                                   uint32_t e0, uint32_t at, uint32_t p) {
+    const uint8_t* c = codes + row * (a.D * Fmt<MODE>::bits / 8u) + e0 * Fmt<MODE>::bits / 8u;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t x = at[tok + u * step][0], y = at[tok + u * step][1];
-      if (c * 32u < D) {  // the same for all units of a thread
-        load_words<4 * words>(codes + (x < 0 ? 0 : x) + c * (4 * words), w[u]);
-        s[u] = load_scales<32 / (int)Fmt<MODE>::group>(scales + (x < 0 ? 0 : y) + c * (32 / Fmt<MODE>::group));
-        if (x < 0) s[u] = 0;
-      } else {
-#pragma unroll
-        for (int i = 0; i < words; ++i) w[u][i] = 0;
-        s[u] = 0;
-      }
+    for (int k = 0; k < pieces; ++k)
+      if (e0 + (uint32_t)k * (128u / Fmt<MODE>::bits) < a.D) cp_async16(at + (k * PROD + p) * 16u, c + 16 * k);
+    const uint64_t off = row * (a.D / Fmt<MODE>::group) + e0 / Fmt<MODE>::group;
+    const uint32_t first = (uint32_t)off & 3u, to = at + S::raw_codes + 8u * p;
+    const uint64_t w = off - first;
+    if (e0 >= a.D) return first;
+    if (w + 8u <= a.scale_bytes) {
+      cp_async4(to, scales + w);
+      if (first + nb > 4u) cp_async4(to + 4u, scales + w + 4u);
+    } else {  // the buffer ends inside the words
+      for (uint32_t i = 0; w + i < a.scale_bytes; ++i) st_shared_u8(to + i, __ldg(scales + w + i));
     }
+    return first;
   }
-  // The units' four octets as 16-byte chunks of the tile.  Units 2, 3 (mod 4)
-  // of a row lie in another box at the same banks as units 0, 1: they store
-  // their octets in another order, so that eight lanes (two rows) always
-  // cover eight chunks.
-  __device__ __forceinline__ void store(uint32_t base, uint32_t tok, uint32_t c) const {
-    const bool swap = per_row >= 4 && (c & 2u);
-    const uint32_t row = base + (tok >> 3) * Shape<DP>::group + (c >> 1) * 1024u + (tok & 7u) * 128u;
-    uint32_t to[4];
+  // Decodes the slots into row `tok` of a tile, elements e0 .. e0 + EPT, as
+  // 16-byte chunks: eight lanes (eight rows) cover eight chunk places.
+  static __device__ __forceinline__ void decode(const AttnArgs& a, uint32_t at, uint32_t p, uint32_t first, bool there, uint32_t tile,
+                                                uint32_t tok, uint32_t e0) {
+    const uint32_t row = tile + (tok >> 3) * S::group + (tok & 7u) * 128u + (e0 >> 6) * 1024u, c0 = (e0 >> 3) & 7u;
+    uint32_t s0, s1;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(at + S::raw_codes + 8u * p));
+    const uint32_t sc = there ? __funnelshift_r(s0, s1, 8u * first) : 0u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      to[e] = row + ((((c & 1u) * 4u + (uint32_t)(swap ? e ^ 2 : e)) ^ (tok & 7u)) << 4);
+    for (int u = 0; u < units; ++u) {
+      if (e0 + 32u * u >= a.D) break;
+      constexpr int wo = (int)Fmt<MODE>::bits / 4;  // words an octet
+      uint32_t w[4 * wo], f[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t f[2];
+      for (int k = 0; k < wo; ++k) {
+        const uint4 v = ld_shared_v4(at + ((u * wo + k) * PROD + p) * 16u);
+        w[4 * k] = v.x;
+        w[4 * k + 1] = v.y;
+        w[4 * k + 2] = v.z;
+        w[4 * k + 3] = v.w;
+      }
       if constexpr (MODE == kNV) {
-        const uint32_t pr = e4m3x2_to_f16x2(s[u]);
-        f[0] = __byte_perm(pr, 0, swap ? 0x3232 : 0x1010);
-        f[1] = __byte_perm(pr, 0, swap ? 0x1010 : 0x3232);
+        const uint32_t pr = e4m3x2_to_f16x2(sc >> (16 * u));
+        f[0] = __byte_perm(pr, 0, 0x1010);
+        f[1] = __byte_perm(pr, 0, 0x3232);
       } else {
-        const uint32_t q = mx_factor<MODE>(s[u]);
+        const uint32_t q = mx_factor<MODE>((sc >> (8 * u)) & 255u);
         f[0] = f[1] = q | (q << 16);
       }
-      uint32_t x[words];
 #pragma unroll
-      for (int i = 0; i < words; ++i) x[i] = swap ? w[u][i ^ (2 * wo)] : w[u][i];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st_shared_v4(to[e] + u * (step / 8u) * Shape<DP>::group, decode8<MODE>(&x[e * wo], f[e / 2]));
+      for (int e = 0; e < 4; ++e)
+        st_shared_v4(row + (((c0 + (u * 4u + e)) ^ (tok & 7u)) << 4), decode8<MODE>(&w[e * wo], f[e / 2]));
     }
   }
 };
@@ -185,6 +242,21 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// Barrier of the two warps that share 32 rows; a warp that gives up arrives
+// without waiting, after it has set the flag that its partner looks at before
+// every further wait.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void pair_leave(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -209,45 +281,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^y of a pair on the FMA pipes: y = n + f with n the nearest integer (from
-// the low bits of y + 1.5 * 2^23), 2^f by the degree-4 polynomial of least
-// relative error on [-1/2, 1/2] (Remez exchange; 2.6e-6, a hundredth of P's
-// rounding), n added to the exponent.  y is raised to -126 first, so nothing
-// wraps; what is masked becomes 2^-126.
-__device__ __forceinline__ uint64_t ex2_poly(uint64_t y2) {
-  float y0, y1;
-  unpair(y2, y0, y1);
-  y2 = pair(fmaxf(y0, -126.0f), fmaxf(y1, -126.0f));
-  const uint64_t big = pair(12582912.0f, 12582912.0f), t = add2(y2, big);
-  const uint64_t f = fma2(add2(t, pair(-12582912.0f, -12582912.0f)), pair(-1.0f, -1.0f), y2);
-  uint64_t p = fma2(f, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
-  p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
-  float t0, t1, p0, p1;
-  unpair(t, t0, t1);
-  unpair(p, p0, p1);
-  return pair(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
-              __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
-}
-
 template <typename QT, int MODE, int DP>
 __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant__ AttnArgs a) {
-  using S = Shape<DP>;
+  using S = Shape<MODE, DP>;
   constexpr int NQ = S::NQ, NT = S::NT;
   constexpr bool kMx = MODE != kNV;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], o_done[2], all_done;
-  __shared__ int64_t rows[2][NT][2];  // byte offsets of the tokens' code and scale rows
+  __shared__ __align__(8) uint64_t full[2][2], empty[2][2], s_full[2], p_full[2], o_done[2], all_done;  // full, empty: [side][stage]
+  __shared__ float other[NQ][2][128];  // maxima (later sums) that the two threads of a row exchange
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_flag;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sq = sbase, sk = sq + NQ * S::q_tile, sv = sk + ST * S::kv_tile;
+  const uint32_t sq = sbase;
   const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31u);
 
-  // heaviest tiles first: the last queries of a causal prompt see most
-  const uint32_t tiles = gridDim.x / a.chunks, tile = tiles - 1u - blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-  const uint32_t hk = blockIdx.y, b = blockIdx.z, r0 = tile * 128u * NQ;
+  // heaviest tiles first, over all heads and sequences: the last queries of a
+  // causal prompt see most
+  const uint32_t per_tile = a.chunks * a.B * a.heads;
+  uint32_t at = blockIdx.x;
+  const uint32_t tile = gridDim.x / per_tile - 1u - at / per_tile;
+  at %= per_tile;
+  const uint32_t chunk = at / (a.B * a.heads);
+  at %= a.B * a.heads;
+  const uint32_t b = at / a.heads, hk = at - b * a.heads, r0 = tile * 128u * NQ;
   Seq s;
   if (!seq_of(a, b, s)) return;
   const uint32_t R = s.n * a.G;
@@ -267,15 +323,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(smem_u32(&k_full[i]), 4);
-      mbar_init(smem_u32(&v_full[i]), 4);
-      mbar_init(smem_u32(&k_empty[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&full[i >> 1][i & 1]), W_MMA);
+      mbar_init(smem_u32(&empty[i >> 1][i & 1]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&p_full[i]), 8);
       mbar_init(smem_u32(&o_done[i]), 1);
     }
     mbar_init(smem_u32(&all_done), 1);
@@ -292,12 +346,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     for (uint32_t pg = pg0 + threadIdx.x; pg <= pg1; pg += THREADS) bad |= (uint32_t)__ldg(table + pg) >= a.num_pages;
     if (bad) atomicOr(&g_device_error, (unsigned)kDevErrIndex);
   }
-  // the query tiles: thread = row
-  const int qt = warp >> 2;  // softmax warps: their query tile
+  // softmax warps: their query tile, half of the tokens, row of the tile
+  const int qt = (warp - W_SOFT) >> 3, half = (warp >> 2) & 1;
   const uint32_t row = (uint32_t)(threadIdx.x & 127u);
   const uint32_t r = r0 + 128u * qt + row;
   float fz = 0.0f;
-  if (warp < 4 * nq) {
+  const bool softmax = warp >= W_SOFT && qt < nq;
+  if (softmax) {  // either thread of a row stores half of it
     const uint32_t i = min(r, R - 1u) / a.G, h = hk * a.G + (min(r, R - 1u) - i * a.G);
     const QT* q = static_cast<const QT*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * a.D;
     float mx = 0.0f;
@@ -311,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     const float up = pow2((kMx ? 40 : 14) - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
     const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
     fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(kMx ? 24 : -14), 1e-37f);
-    for (uint32_t o = 0; o < a.D / 8u; ++o) {
+    for (uint32_t o = half; o < a.D / 8u; o += 2u) {
       float x[8];
       load8<QT>(q + 8u * o, x);
       uint32_t v[4];
@@ -330,57 +385,55 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
 
-  if (warp >= W_PROD && warp < W_MMA) {
+  if (warp < W_MMA) {
     // ------------------------------------------------------------ producers
-    const uint32_t p = (uint32_t)(threadIdx.x - 32 * W_PROD);
-    // Rows of tile n's tokens; true on every producer once any has given up.
-    auto look = [&](int32_t n) {
-      if (n < iters && p < (uint32_t)NT) {
-        const int32_t j = begin + n * NT + (int32_t)p;
-        int64_t x = -1;
-        if (j >= rg.lo && j < end) {
-          const uint32_t pg = a.by_page.div((uint32_t)j);
-          const int32_t page = __ldg(table + pg);
-          if ((uint32_t)page < a.num_pages)
-            x = (int64_t)(((uint64_t)page * a.heads + hk) * a.page_size + ((uint32_t)j - pg * a.page_size));
-        }
-        rows[n & 1][p][0] = x * (int64_t)(a.D * Fmt<MODE>::bits / 8u);
-        rows[n & 1][p][1] = x * (int64_t)(a.D / Fmt<MODE>::group);
-      }
-      uint32_t stop;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-          "barrier.cta.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(stop)
-          : "r"((uint32_t)abort_flag)
-          : "memory");
-      return stop != 0;
+    using W = Raw<MODE, DP>;
+    const uint32_t p = threadIdx.x, tok = p % NT, e0 = p / NT * S::EPT;
+    // tile n's token: its page number is loaded a tile before its row is
+    // wanted, its codes and scales a tile before they are decoded
+    int32_t page = -1;
+    auto page_of = [&](int32_t n) {
+      const int32_t j = begin + n * NT + (int32_t)tok;
+      page = n < iters && j >= rg.lo && j < end ? __ldg(table + a.by_page.div((uint32_t)j)) : -1;
     };
-    using Sh = Share<MODE, DP>;
-    Sh kk, vv;
-    const uint32_t tok = p / Sh::per_row, c = p % Sh::per_row;
-    look(0);
-    if (iters > 0) {
-      kk.load(a.codes[0], a.scales[0], rows[0], tok, c, a.D);
-      vv.load(a.codes[1], a.scales[1], rows[0], tok, c, a.D);
-    }
-    look(1);
-    for (int32_t n = 0; n < iters; ++n) {
-      const uint32_t st = (uint32_t)n % ST, ph = ((uint32_t)n / ST) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&k_empty[st]), ph ^ 1u)) || abort_flag) abort_flag = 1;
-      kk.store(sk + st * S::kv_tile, tok, c);
+    uint64_t row = 0;
+    bool there = false;
+    auto fetch = [&](int32_t q) {  // tile q / 2, side q % 2
+      const int32_t n = q >> 1;
+      uint32_t first = 0;
+      if (n < iters) {
+        if ((q & 1) == 0) {
+          const uint32_t j = (uint32_t)(begin + n * NT) + tok;
+          there = (uint32_t)page < a.num_pages;
+          row = there ? ((uint64_t)(uint32_t)page * a.heads + hk) * a.page_size + (j - a.by_page.div(j) * a.page_size) : 0;
+          page_of(n + 1);
+        }
+        // a token that is not there gets row 0's codes, and zero scales when decoded (finite: P = 0 meets them)
+        first = W::fetch(a, q & 1 ? a.codes[1] : a.codes[0], q & 1 ? a.scales[1] : a.scales[0], row, e0, sbase + S::at_raw + (q & 1) * S::raw, p) | (there ? 4u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return first;
+    };
+    page_of(0);
+    uint32_t cur = fetch(0), next = fetch(1);
+#pragma unroll 1
+    for (int32_t q = 0; q < 2 * iters; ++q) {
+      const uint32_t side = (uint32_t)q & 1u, n = (uint32_t)q >> 1, nst = side ? S::st_v : S::st_k;
+      const uint32_t st = n % nst, ph = n / nst & 1u;
+      if (!__all_sync(0xffffffffu, wait_for(empty[side][st], ph ^ 1u) && !abort_flag)) {
+        abort_flag = 1;
+        break;
+      }
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      W::decode(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile,
+                tok, e0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive(smem_u32(&k_full[st]));
-      if (n + 1 < iters) kk.load(a.codes[0], a.scales[0], rows[(n + 1) & 1], tok, c, a.D);
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&v_empty[st]), ph ^ 1u)) || abort_flag) abort_flag = 1;
-      vv.store(sv + st * S::kv_tile, tok, c);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(smem_u32(&v_full[st]));
-      if (n + 1 < iters) vv.load(a.codes[1], a.scales[1], rows[(n + 1) & 1], tok, c, a.D);
-      if (look(n + 2)) break;  // rows[n & 1]: every thread read it for tile n before the last look
+      if (lane == 0) arrive(smem_u32(&full[side][st]));
+      cur = next;
+      next = fetch(q + 2);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
@@ -389,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     auto qk = [&](int t, int32_t n) {
       if (leader) {
         const uint64_t da = smem_desc(sq + t * S::q_tile, 16, S::group, 2);
-        const uint64_t db = smem_desc(sk + ((uint32_t)n % ST) * S::kv_tile, 16, S::group, 2);
+        const uint64_t db = smem_desc(sbase + S::at_k + ((uint32_t)n % S::st_k) * S::kv_tile, 16, S::group, 2);
         for (uint32_t j = 0; j < kchunks; ++j) {
           const uint64_t off = ((j >> 2) * 1024u + (j & 3u) * 32u) >> 4;
           mma_ss(tmem + S::tm_s + 128u * t, da + off, db + off, id_qk, j != 0);
@@ -399,41 +452,42 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       __syncwarp();
     };
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity)) && !abort_flag;
+      ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity) && !abort_flag);
       tc_fence_after();
       return ok;
     };
-    if (iters > 0 && wait(k_full[0], 0)) {
+    if (iters > 0 && wait(full[0][0], 0)) {
       for (int t = 0; t < nq; ++t) qk(t, 0);
-      if (leader) mma_commit(smem_u32(&k_empty[0]));
+      if (leader) mma_commit(smem_u32(&empty[0][0]));
     }
     for (int32_t n = 0; n < iters && ok; ++n) {
-      const uint32_t st = (uint32_t)n % ST, ph = ((uint32_t)n / ST) & 1u;
+      const uint32_t st = (uint32_t)n % S::st_v, ph = ((uint32_t)n / S::st_v) & 1u;
       for (int t = 0; t < nq && ok; ++t) {
-        if (t == 0 && !wait(v_full[st], ph)) break;
+        if (t == 0 && !wait(full[1][st], ph)) break;
         if (!wait(p_full[t], (uint32_t)n & 1u)) break;
         if (leader) {
-          const uint64_t db = smem_desc(sv + st * S::kv_tile, 1024, S::group, 2);
+          const uint64_t db = smem_desc(sbase + S::at_v + st * S::kv_tile, 1024, S::group, 2);
           const uint32_t pa = tmem + S::tm_s + 128u * t, od = tmem + S::tm_o + 128u * t;
           for (uint32_t j = 0; j < NT / 16; ++j) {
             const uint64_t bj = db + ((j * 2u * S::group) >> 4);
+            const uint32_t ph = pa + S::HC * (j / (S::HC / 16u)), jh = j % (S::HC / 16u);  // P lies in its half of S
             if constexpr (!kMx) {
-              mma_ts(od, pa + 8u * j, bj, id_pv, (n | (int32_t)j) != 0);
+              mma_ts(od, ph + 8u * jh, bj, id_pv, (n | (int32_t)j) != 0);
             } else {
-              const uint32_t pj = pa + 32u * (j >> 1) + 8u * (j & 1u);
+              const uint32_t pj = ph + 32u * (jh >> 1) + 8u * (jh & 1u);
               mma_ts(od, pj, bj, id_pv, (n | (int32_t)j) != 0);
               mma_ts(od, pj + 16u, bj, id_pv, 1);
             }
           }
           mma_commit(smem_u32(&o_done[t]));
-          if (t == nq - 1) mma_commit(smem_u32(&v_empty[st]));
+          if (t == nq - 1) mma_commit(smem_u32(&empty[1][st]));
         }
         __syncwarp();
         if (n + 1 < iters) {
-          const uint32_t sn = (uint32_t)(n + 1) % ST;
-          if (t == 0 && !wait(k_full[sn], ((uint32_t)(n + 1) / ST) & 1u)) break;
+          const uint32_t sn = (uint32_t)(n + 1) % S::st_k;
+          if (t == 0 && !wait(full[0][sn], ((uint32_t)(n + 1) / S::st_k) & 1u)) break;
           qk(t, n + 1);
-          if (t == nq - 1 && leader) mma_commit(smem_u32(&k_empty[sn]));
+          if (t == nq - 1 && leader) mma_commit(smem_u32(&empty[0][sn]));
         }
         __syncwarp();
       }
@@ -442,85 +496,92 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     // every MMA issued here has completed before TMEM is released
     if (leader) mma_commit(smem_u32(&all_done));
     __syncwarp();
-    mbar_wait(smem_u32(&all_done), 0);
-  } else if (warp < 4 * nq) {
+    wait_for(all_done, 0);
+  } else if (softmax) {
     // ------------------------------------------------------------ softmax
     const uint32_t tl = tmem + ((32u * ((uint32_t)warp & 3u)) << 16);
-    const uint32_t ts_ = tl + S::tm_s + 128u * qt, to = tl + S::tm_o + 128u * qt;
+    const uint32_t ts_ = tl + S::tm_s + 128u * qt + S::HC * half, to = tl + S::tm_o + 128u * qt;
     const uint32_t i = min(r, R - 1u) / a.G;
     const Range see = tile_range(a, s, i, i);
     const uint32_t f0 = r0 + 128u * qt, f1 = min(f0 + 127u, R - 1u);
     const int32_t all_lo = tile_range(a, s, f1 / a.G, f1 / a.G).lo, all_hi = min(end, tile_range(a, s, f0 / a.G, f0 / a.G).hi);
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    auto leave = [&]() {
+      abort_flag = 1;
+      __threadfence_block();
+      pair_leave(2 + 4 * qt + (warp & 3));
+      return false;
+    };
     for (int32_t n = 0; n < iters; ++n) {
-      const int32_t j0 = begin + n * NT;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[qt]), (uint32_t)n & 1u)) || abort_flag) {
-        ok = false;
+      const int32_t j0 = begin + n * NT + S::HC * half;
+      if (!__all_sync(0xffffffffu, wait_for(s_full[qt], (uint32_t)n & 1u) && !abort_flag)) {
+        ok = leave();
         break;
       }
       tc_fence_after();
-      const bool masked = any_bad || j0 < all_lo || j0 + NT > all_hi;
-      constexpr int NC = NT / 32;
-      uint32_t x[2][32];
-      if (masked) {  // minus infinity into S itself; few tiles have a border
+      constexpr int NC = S::HC / 32;
+      uint32_t x[32];
+      if (any_bad || j0 < all_lo || j0 + S::HC > all_hi) {  // minus infinity into S itself; few tiles have a border
 #pragma unroll 1
         for (int c = 0; c < NC; ++c) {
-          tmem_ld32_start(ts_ + 32u * c, x[0]);
-          tmem_ld32_wait(x[0]);
+          tmem_ld32_start(ts_ + 32u * c, x);
+          tmem_ld32_wait(x);
           const int32_t jc = j0 + 32 * c;
           const int32_t lo = see.lo - jc, hi = min(see.hi, end) - jc;
           uint32_t in = (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u) & (hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u);
           if (any_bad)
             for (int e = 0; e < 32; ++e)
               if (((in >> e) & 1u) && (uint32_t)__ldg(table + a.by_page.div((uint32_t)(jc + e))) >= a.num_pages) in &= ~(1u << e);
-          uint32_t y[2][16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e / 16][e % 16] = (in >> e) & 1u ? x[0][e] : 0xFF800000u;
-          tmem_st<16>(ts_ + 32u * c, y[0]);
-          tmem_st<16>(ts_ + 32u * c + 16u, y[1]);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = (in >> (16 * k + e)) & 1u ? x[16 * k + e] : 0xFF800000u;
+            tmem_st<16>(ts_ + 32u * c + 16u * k, y);
+          }
         }
         tmem_wait_st();
       }
       float top;
-      tmem_ld32_start(ts_, x[0]);
       {
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          tmem_ld32_wait(x[c & 1]);
-          if (c + 1 < NC) tmem_ld32_start(ts_ + 32u * (c + 1), x[(c + 1) & 1]);
+          tmem_ld32_start(ts_ + 32u * c, x);
+          tmem_ld32_wait(x);
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              t4[k] = max3(t4[k], __uint_as_float(x[c & 1][e + 2 * k]), __uint_as_float(x[c & 1][e + 2 * k + 1]));
+            for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
         }
         top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       }
-      tmem_ld32_start(ts_, x[0]);
-      top = top * fz - (kMx ? 32.0f : 0.0f);
+      tmem_ld32_start(ts_, x);
+      // the row's other thread has the other half's maximum
+      // (its slot was read before the P that this S followed)
+      other[qt][half][row] = top;
+      pair_sync(2 + 4 * qt + (warp & 3));
+      top = fmaxf(top, other[qt][half ^ 1][row]) * fz - (kMx ? 32.0f : 0.0f);
+      tmem_ld32_wait(x);
       // the reference moves only when exceeded by 2^8 (see k_kv_decode)
       if (__any_sync(0xffffffffu, top > m + 8.0f)) {
         const float mn = fmaxf(m, top);
         const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
         m = mn;
         l *= f;
-        if (n > 0) {  // O as of the previous tile
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[qt]), (uint32_t)(n - 1) & 1u))) {
-            ok = false;
+        if (n > 0) {  // O as of the previous tile, half of the columns each
+          if (!__all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(n - 1) & 1u))) {
+            ok = leave();
             break;
           }
           tc_fence_after();
-          tmem_ld32_wait(x[0]);  // the load above ends before x[1] waits for others
-          for (uint32_t c = 0; c < a.D; c += 32u) {
-            tmem_ld32_start(to + c, x[1]);
-            tmem_ld32_wait(x[1]);
-            uint32_t y[2][16];
+          for (uint32_t c = 16u * half; c < a.D; c += 32u) {
+            uint32_t y[16];
+            tmem_ld16(to + c, y);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e / 16][e % 16] = __float_as_uint(__uint_as_float(x[1][e]) * f);
-            tmem_st<16>(to + c, y[0]);
-            tmem_st<16>(to + c + 16u, y[1]);
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+            tmem_st<16>(to + c, y);
           }
           tmem_wait_st();
         }
@@ -528,22 +589,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       const float ref = m == -INFINITY ? 0.0f : m;
       const uint64_t fz2 = pair(fz, fz), ref2 = pair(-ref, -ref);
       uint64_t l2[2] = {0, 0};
-      auto weights = [&](int c, const uint32_t (&z)[32]) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (c > 0) {
+          tmem_ld32_start(ts_ + 32u * c, x);
+          tmem_ld32_wait(x);
+        }
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          uint64_t y = fma2(pair(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])), fz2, ref2);
+          const uint64_t y = fma2(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), fz2, ref2);
           float p0, p1;
-          if (e % kPolyEvery == kPolyEvery - 1) {
-            y = ex2_poly(y);
-            unpair(y, p0, p1);
-          } else {
-            unpair(y, p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            y = pair(p0, p1);
-          }
-          l2[e & 1] = add2(l2[e & 1], y);
+          unpair(y, p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
           if constexpr (!kMx) {
             hi[e] = pack_f16x2(p0, p1);
           } else {
@@ -557,15 +617,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
           tmem_st<16>(ts_ + 32u * c, hi);
           tmem_st<16>(ts_ + 32u * c + 16u, lo);
         }
-      };
-#pragma unroll 1  // twice NC / 2: the loop body stays in the instruction cache
-      for (int c = 0; c < NC; c += 2) {
-        tmem_ld32_wait(x[0]);
-        tmem_ld32_start(ts_ + 32u * (c + 1), x[1]);
-        weights(c, x[0]);
-        tmem_ld32_wait(x[1]);
-        if (c + 2 < NC) tmem_ld32_start(ts_ + 32u * (c + 2), x[0]);
-        weights(c + 1, x[1]);
       }
       {
         float s0, s1;
@@ -578,35 +629,38 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       if (lane == 0) arrive(smem_u32(&p_full[qt]));
     }
     if (ok && iters > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[qt]), (uint32_t)(iters - 1) & 1u)) && !abort_flag;
+      ok = __all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(iters - 1) & 1u) && !abort_flag);
       tc_fence_after();
     }
     if (!ok) {
       if (lane == 0) abort_flag = 1;
     } else {
+      // the row's sum (the slots were last read before the last P)
+      other[qt][half][row] = l;
+      pair_sync(2 + 4 * qt + (warp & 3));
+      l += other[qt][half ^ 1][row];
       const uint32_t h = hk * a.G + (min(r, R - 1u) - i * a.G);
       const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
       const float fv = kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
-      if (m == -INFINITY) l = 0.0f;  // nothing seen (ex2_poly leaves 2^-126)
       const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
-      if (r < R) {
+      if (r < R && half == 0) {
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);
         else if (a.lse) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
-      for (uint32_t c = 0; c < a.D; c += 32u) {
-        float x[32];
+      for (uint32_t c = 16u * half; c < a.D; c += 32u) {
+        uint32_t y[16];
         if (iters > 0) {
-          tmem_ld32(to + c, x);
+          tmem_ld16(to + c, y);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.0f;
+          for (int e = 0; e < 16; ++e) y[e] = 0;
         }
         if (r < R)
 #pragma unroll
-          for (int o = 0; o < 4; ++o) {
+          for (int o = 0; o < 2; ++o) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[octet<MODE>(e)] = x[8 * o + e] * f;
+            for (int e = 0; e < 8; ++e) v[octet<MODE>(e)] = __uint_as_float(y[8 * o + e]) * f;
             if (whole)
               store8<QT>(static_cast<QT*>(a.out) + at * a.D + c + 8 * o, v);
             else

@@ -1035,8 +1035,9 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.page_size = (uint32_t)cache->page_size;
   a.window = window > (1 << 30) ? 0u : (uint32_t)window;  // a window past any length hides nothing
   a.causal = causal != 0;
+  a.scale_bytes = (uint64_t)cache->num_pages * cache->heads * cache->page_size * (cache->D / (cache->mode == NVFP4_MODE_NVFP4 ? 16 : 32));
   a.by_page.init(a.page_size);
-  // k_kv_prefill: no two-term Q for fp16 over the MX modes; it loads some row
+  // k_kv_prefill: no two-term Q for fp16 over the MX modes; it copies some row
   // for every token, so there has to be one
   const bool prefill_has_it = (cache->mode == NVFP4_MODE_NVFP4 || q_dt == NVFP4_DT_BF16) && cache->num_pages > 0;
   const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, prefill_has_it, workspace_bytes);
@@ -1047,7 +1048,9 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (size_t)p.chunks * T * Hq * cache->D * 4);
   const int64_t tiles = (max_q * a.G + p.tile_rows - 1) / p.tile_rows;
   if (product_exceeds(tiles, p.chunks, INT32_MAX)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q and max_kv too large", tag);
-  const dim3 grid((unsigned)(tiles * p.chunks), a.heads, a.B);
+  if (p.prefill && product_exceeds(tiles * p.chunks, B * cache->heads, INT32_MAX))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q, max_kv and B too large together", tag);
+  const dim3 grid = p.prefill ? dim3((unsigned)(tiles * p.chunks * B * cache->heads)) : dim3((unsigned)(tiles * p.chunks), a.heads, a.B);
   const bool one_page = a.page_size % 16 == 0 && !product_exceeds(cache->num_pages * cache->page_size, cache->heads, UINT32_MAX);
   cudaError_t e = cudaSuccess;
   dispatch_mode(cache->mode, [&](auto m) {
@@ -1059,8 +1062,8 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
         if (p.prefill) {
           if constexpr (MODE == kv::kNV || std::is_same<QT, __nv_bfloat16>::value) {
             auto kern = kv::pf::k_kv_prefill<QT, MODE, DP>;
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv::pf::Shape<DP>::smem);
-            if (e == cudaSuccess) kern<<<grid, kv::pf::THREADS, kv::pf::Shape<DP>::smem, stream>>>(a);
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv::pf::Shape<MODE, DP>::smem);
+            if (e == cudaSuccess) kern<<<grid, kv::pf::THREADS, kv::pf::Shape<MODE, DP>::smem, stream>>>(a);
           }
           return;
         }
