@@ -31,12 +31,14 @@ struct AttnArgs {
   uint32_t B, T, Hq, heads, G, D, max_q, max_kv, max_pages, num_pages, page_size;
   uint32_t window;              // 0: none
   int causal;
-  int32_t chunk;                // tokens a CTA walks (a multiple of 16, at most 2^30)
+  int32_t chunk;                // k_kv_prefill: tokens a CTA walks (a multiple of 16, at most 2^30)
   uint32_t chunks;              // CTAs a row tile has
   uint32_t tile_rows;           // query rows a CTA holds
+  int split;                    // k_kv_decode: 0 where there is no workspace
   uint64_t scale_bytes;         // of one side
-  float2* part_ml;              // [chunks, T, Hq]
-  float* part_o;                // [chunks, T, Hq, D]
+  float2* part_ml;              // [chunks, T, Hq]; k_kv_decode: [workers, 2, rows]
+  float* part_o;                // [chunks, T, Hq, D]; [workers, 2, rows, D]
+  int4* part_head;              // k_kv_decode: [workers]
   FastDiv by_page;
 };
 
@@ -63,14 +65,12 @@ __device__ __forceinline__ bool seq_of(const AttnArgs& a, uint32_t b, Seq& s) {
 }
 
 // ---------------------------------------------------------------------------
-// Split work and partial results
+// Ranges and partial results
 // ---------------------------------------------------------------------------
-// The tokens any of a row tile's queries can see are the range [lo, hi); it
-// is walked in chunks of `chunk` tokens counted from lo rounded down to 16.
-// A tile whose range takes one chunk is finished by its CTA; otherwise chunk c
-// leaves (m, l, O) of every row -- O = sum 2^(z_j - m) v_j, l = sum
-// 2^(z_j - m), logits z in units of log2 -- at index (c, t, h) of the
-// partials, and k_kv_join adds them up.
+// The tokens any of a row tile's queries can see are the range [lo, hi).
+// Where several CTAs walk one range, each leaves (m, l, O) of every row --
+// O = sum 2^(z_j - m) v_j, l = sum 2^(z_j - m), logits z in units of log2 --
+// and a second kernel adds them up.
 struct Range {
   int32_t lo, hi;  // hi <= lo: nothing
 };
@@ -98,12 +98,23 @@ __device__ __forceinline__ float ex2(float x) {
 // Few query rows: k_kv_decode
 // ---------------------------------------------------------------------------
 // The R = n * G rows (queries x heads of one group) of a sequence and a
-// key/value head, 8 * NT of them a CTA; four warps take steps of 16 * TS
-// tokens in turn, each with its own running maximum, and join at the end.
-// Codes go from global memory straight into matrix fragments: a quad of lanes
-// loads one token's key row (the order of the elements along D is free as
-// long as q's fragments use the same), and a lane's share of a value row is
-// the D / 8 consecutive elements of its fragment rows.
+// key/value head are cut into tiles of 8 * NT; a tile walks its tokens in
+// units of 64 * TS.  All units of all (sequence, tile, head) in that order
+// are dealt out in equal runs to as many CTAs as fit the GPU at once, so
+// uneven lengths, few heads and one long sequence fill the SMs alike (with a
+// grid of equal chunks the last wave stood half empty: one sequence of
+// 131072 tokens took 55 us in 2.4 waves, 47 us in one).  A run begins and
+// ends anywhere in a range: what it does not cover whole goes to k_kv_join.
+//
+// In a CTA a fifth warp copies the units ahead into shared memory with bulk
+// copies (one a page, or a 16-token piece of one, and part: K and V codes, K
+// and V scales), so loads cost the other four neither instructions nor
+// registers; each of those takes 16 * TS tokens of every unit, with its own
+// running maximum, and they join at the end of a range.  Codes go from shared
+// memory straight into matrix fragments: a quad of lanes holds one token's
+// key row (the order of the elements along D is free as long as q's fragments
+// use the same), and a lane's share of a value row is the D / 8 consecutive
+// elements of its fragment rows.
 //   S^T [16 tokens x 8 rows] = K_hat . q^T      (m16n8k16, fp32)
 //   O^T [16 elements x 8 rows] += V_hat^T . P^T
 // P^T is S^T's fragment transposed by movmatrix.
@@ -119,7 +130,7 @@ __device__ __forceinline__ float ex2(float x) {
 // to [2^40, 2^41) and split into two bf16 terms when it is fp16 (11 bits = 8
 // + 3), and P, scaled by 2^32, into two bf16 terms (16 bits), so nothing
 // rounds to fewer bits than fp16 would.
-enum { kDecWarps = 4, kDecThreads = kDecWarps * 32 };
+enum { kDecWarps = 4, kDecThreads = (kDecWarps + 1) * 32 };
 
 template <int MODE, int DP>
 struct Geo {
@@ -127,7 +138,11 @@ struct Geo {
   static constexpr int vbytes = DP / 8 * (int)Fmt<MODE>::bits / 8, vw = vbytes / 4;  // and of a value row
   static constexpr int ksteps = DP / 16, mtiles = DP / 16;
   static constexpr int krow = DP * (int)Fmt<MODE>::bits / 8, srow = DP / (int)Fmt<MODE>::group;  // a row's bytes
-  static constexpr int ts = (MODE == kMX8 || DP == 256) ? 1 : 2;  // 16-token tiles a step: what 255 registers hold
+  // 16-token tiles of a warp in a unit, units in shared memory: about 64 KB a
+  // CTA, three CTAs an SM
+  static constexpr int ts = DP == 256 || (MODE == kMX8 && DP == 128) ? 1 : 2;
+  static constexpr int unit = 16 * kDecWarps * ts, unit_bytes = 2 * unit * (krow + srow);
+  static constexpr int stages = unit_bytes > 26000 ? 2 : unit_bytes > 12000 ? 3 : 4;
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -200,15 +215,15 @@ __device__ __forceinline__ uint32_t mx_factor(uint32_t s) {
 template <int BYTES>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (BYTES == 4) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (BYTES == 8) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
       w[4 * i] = v.x;
       w[4 * i + 1] = v.y;
       w[4 * i + 2] = v.z;
@@ -220,67 +235,13 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 // N scale bytes (N < 1: the byte that several lanes share).
 template <int N>
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
-  if constexpr (N <= 1) return __ldg(p);
-  else if constexpr (N == 2) return __ldg(reinterpret_cast<const uint16_t*>(p));
-  else return __ldg(reinterpret_cast<const uint32_t*>(p));
+  if constexpr (N <= 1) return *p;
+  else if constexpr (N == 2) return *reinterpret_cast<const uint16_t*>(p);
+  else return *reinterpret_cast<const uint32_t*>(p);
 }
 
-// A lane's key words and scales of one token row; `row` < 0 gives zeros.
-// 32 elements (one piece) is what D is a multiple of.
-template <int MODE, int DP>
-__device__ __forceinline__ void load_key(const AttnArgs& a, int64_t row, uint32_t c, uint32_t* w, uint32_t& sc) {
-  using G = Geo<MODE, DP>;
-  constexpr uint32_t bits = Fmt<MODE>::bits, group = Fmt<MODE>::group, per = DP / 4;
-  constexpr int piece = G::kbytes < (int)(4 * bits) ? G::kbytes : (int)(4 * bits);  // bytes of at most 32 elements
-#pragma unroll
-  for (int i = 0; i < G::kw; ++i) w[i] = 0;
-  sc = 0;
-  if (row < 0) return;
-  const uint8_t* p = a.codes[0] + (uint64_t)row * (a.D * bits / 8u) + c * G::kbytes;
-#pragma unroll
-  for (int i = 0; i < G::kbytes / piece; ++i)
-    if (c * per + 32u * i < a.D) load_words<piece>(p + i * piece, w + i * (piece / 4));
-  const uint8_t* s = a.scales[0] + (uint64_t)row * (a.D / group);
-  if constexpr (MODE == kNV) {
-    if constexpr (DP == 64) {
-      if (16u * c < a.D) sc = __ldg(s + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < DP / 128; ++i)
-        if (c * per + 32u * i < a.D)
-          sc |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(s + c * (per / 16)) + i) << (16 * i);
-    }
-  } else if constexpr (DP == 64) {
-    if (16u * c < a.D) sc = __ldg(s + c / 2);
-  } else {
-#pragma unroll
-    for (int i = 0; i < DP / 128; ++i)
-      if (c * per + 32u * i < a.D) sc |= (uint32_t)__ldg(s + c * (DP / 128) + i) << (8 * i);
-  }
-}
-
-// A lane's value words and scales (byte 0, and byte 1 for a second block) of
-// one token row.
-template <int MODE, int DP>
-__device__ __forceinline__ void load_value(const AttnArgs& a, int64_t row, uint32_t g, uint32_t* w, uint32_t& sc) {
-  using G = Geo<MODE, DP>;
-  constexpr uint32_t bits = Fmt<MODE>::bits, group = Fmt<MODE>::group, per = DP / 8;
-#pragma unroll
-  for (int i = 0; i < G::vw; ++i) w[i] = 0;
-  sc = 0;
-  if (row < 0 || g * per >= a.D) return;
-  load_words<G::vbytes>(a.codes[1] + (uint64_t)row * (a.D * bits / 8u) + g * G::vbytes, w);
-  const uint8_t* s = a.scales[1] + (uint64_t)row * (a.D / group);
-  if constexpr (MODE == kNV && DP == 256)
-    sc = __ldg(reinterpret_cast<const uint16_t*>(s) + g);
-  else
-    sc = __ldg(s + g * per / group);
-}
-
-// FAST: D == DP, 16-token tiles lie on one page and rows have 32-bit numbers;
-// a step wholly inside the range then loads without a check at fixed offsets
-// from one row.  Everything else looks each row up.
-template <typename QT, int MODE, int DP, int NT, bool FAST>
+// EXACT: D == DP; otherwise a row's elements beyond D read as zero.
+template <typename QT, int MODE, int DP, int NT, bool EXACT>
 struct Decode {
   using G = Geo<MODE, DP>;
   static constexpr int TS = G::ts;
@@ -291,8 +252,8 @@ struct Decode {
   float fz[NT][2];     // logit (log2 units) of an accumulator, for this lane's two columns
   float m[NT][2], l[NT][2];
   float o[NT][G::mtiles][4];
-  uint32_t kw[TS][2][G::kw], ks[TS][2], vw[TS][4][G::vw], vs[TS][4];
   uint32_t lane, g, c;
+  uint32_t rb, sb, D;  // a row's code and scale bytes, elements
 
   // Element (within the lane's DP / 4) of k-step s, fragment register j, half e.
   __device__ static constexpr int q_elem(int s, int j, int e) {
@@ -349,72 +310,44 @@ struct Decode {
     }
   }
 
-  // Row of token j, or -1 where it is outside [lo, hi) or its page is not one.
-  __device__ __forceinline__ int64_t row_at(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j, const Range& rg) const {
-    if (j < rg.lo || j >= rg.hi) return -1;
-    const uint32_t pg = a.by_page.div((uint32_t)j);
-    const int32_t page = __ldg(table + pg);
-    if (page < 0 || (uint32_t)page >= a.num_pages) {
-      atomicOr(&g_device_error, (unsigned)kDevErrIndex);
-      return -1;
-    }
-    return (int64_t)(((uint64_t)page * a.heads + hk) * a.page_size + ((uint32_t)j - pg * a.page_size));
-  }
-  // FAST: row of token 0 of a 16-token tile on page `page`.
-  __device__ __forceinline__ uint32_t tile_row(const AttnArgs& a, int32_t page, uint32_t hk, int32_t j0) const {
-    return ((uint32_t)page * a.heads + hk) * a.page_size + ((uint32_t)j0 - a.by_page.div((uint32_t)j0) * a.page_size);
-  }
+  // Fragment row r of a 16-token tile is token r with the last bit turned over
+  // where bit 1 is set: a lane column's value rows then lie on both halves of
+  // the banks.
+  __device__ __forceinline__ static uint32_t token(uint32_t r) { return r ^ ((r >> 1) & 1u); }
+  __device__ __forceinline__ uint32_t row_bytes() const { return EXACT ? (uint32_t)G::krow : rb; }
+  __device__ __forceinline__ uint32_t scale_bytes() const { return EXACT ? (uint32_t)G::srow : sb; }
 
-  // Bit 2t + i of the result: token 16 t + 8 i + g of the step is there.
-  __device__ __forceinline__ uint32_t load_keys(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j0, const Range& rg,
-                                                bool inside, const uint32_t (&rows)[TS]) {
-    if (FAST && inside) {
+  // This lane's key words and scales of token `tok` of a unit.
+  __device__ __forceinline__ void load_key(const uint8_t* codes, const uint8_t* scales, uint32_t tok, uint32_t (&w)[G::kw], uint32_t& sc) const {
+    constexpr uint32_t per = DP / 4, group = Fmt<MODE>::group;
+    const uint8_t* p = codes + tok * row_bytes() + c * G::kbytes;
+    const uint8_t* q = scales + tok * scale_bytes() + c * per / group;
+    if constexpr (EXACT) {
+      load_words<G::kbytes>(p, w);
+      sc = load_scales<per / group>(q);
+    } else {
+      constexpr int piece = per < 32 ? G::kbytes : 4 * (int)Fmt<MODE>::bits;  // bytes of at most 32 elements
 #pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        const uint8_t* p = a.codes[0] + (uint64_t)(rows[t] + g) * G::krow + c * G::kbytes;
-        const uint8_t* q = a.scales[0] + (uint64_t)(rows[t] + g) * G::srow + c * (DP / 4) / Fmt<MODE>::group;
+      for (int i = 0; i < G::kw; ++i) w[i] = 0;
+      sc = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          load_words<G::kbytes>(p + 8 * i * G::krow, kw[t][i]);
-          ks[t][i] = load_scales<DP / 4 / Fmt<MODE>::group>(q + 8 * i * G::srow);
+      for (int i = 0; i < G::kbytes / piece; ++i)
+        if (c * per + 32u * i < D) {
+          load_words<piece>(p + i * piece, w + i * (piece / 4));
+          constexpr int n = per < 32 ? per / group : 32 / group;  // its scales
+          sc |= load_scales<n>(q + i * (32 / group)) << (8 * i * (32 / group));
         }
-      }
-      return (1u << (2 * TS)) - 1u;
     }
-    uint32_t there = 0;
-#pragma unroll
-    for (int t = 0; t < TS; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t row = row_at(a, table, hk, j0 + 16 * t + 8 * i + g, rg);
-        there |= (row >= 0 ? 1u : 0u) << (2 * t + i);
-        load_key<MODE, DP>(a, row, c, kw[t][i], ks[t][i]);
-      }
-    return there;
   }
-  __device__ __forceinline__ void load_values(const AttnArgs& a, const int32_t* table, uint32_t hk, int32_t j0, const Range& rg,
-                                              bool inside, const uint32_t (&rows)[TS]) {
-    if (FAST && inside) {
+  // And value words and scales (byte 0, and byte 1 for a second block).
+  __device__ __forceinline__ void load_value(const uint8_t* codes, const uint8_t* scales, uint32_t tok, uint32_t (&w)[G::vw], uint32_t& sc) const {
+    constexpr uint32_t per = DP / 8, group = Fmt<MODE>::group;
 #pragma unroll
-      for (int t = 0; t < TS; ++t) {
-        const uint8_t* p = a.codes[1] + (uint64_t)(rows[t] + 2 * c) * G::krow + g * G::vbytes;
-        const uint8_t* q = a.scales[1] + (uint64_t)(rows[t] + 2 * c) * G::srow + g * (DP / 8) / Fmt<MODE>::group;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = (i & 1) + 8 * (i >> 1);
-          load_words<G::vbytes>(p + x * G::krow, vw[t][i]);
-          vs[t][i] = load_scales<DP / 8 / Fmt<MODE>::group>(q + x * G::srow);
-        }
-      }
-      return;
-    }
-#pragma unroll
-    for (int t = 0; t < TS; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = row_at(a, table, hk, j0 + 16 * t + 2 * c + (i & 1) + 8 * (i >> 1), rg);
-        load_value<MODE, DP>(a, row, g, vw[t][i], vs[t][i]);
-      }
+    for (int i = 0; i < G::vw; ++i) w[i] = 0;
+    sc = 0;
+    if (!EXACT && g * per >= D) return;
+    load_words<G::vbytes>(codes + tok * row_bytes() + g * G::vbytes, w);
+    sc = load_scales<per / group>(scales + tok * scale_bytes() + g * per / group);
   }
 
   __device__ __forceinline__ void step_mma(float (&s)[NT][4], int ks_, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -429,8 +362,11 @@ struct Decode {
     }
   }
 
-  // S^T of tile t.
-  __device__ __forceinline__ void logits(int t, float (&s)[NT][4]) {
+  // S^T of the tile at token `tok0` of a unit.
+  __device__ __forceinline__ void logits(const uint8_t* codes, const uint8_t* scales, uint32_t tok0, float (&s)[NT][4]) {
+    uint32_t kw[2][G::kw], ks[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_key(codes, scales, tok0 + token(g) + 8u * i, kw[i], ks[i]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -441,15 +377,15 @@ struct Decode {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int b = 0; b < DP / 64; b += 2) {
-          const uint32_t p = e4m3x2_to_f16x2(ks[t][i] >> (8 * b));
+          const uint32_t p = e4m3x2_to_f16x2(ks[i] >> (8 * b));
           sc[i][b] = __byte_perm(p, 0, 0x1010);
           if (b + 1 < DP / 64) sc[i][b + 1] = __byte_perm(p, 0, 0x3232);
         }
 #pragma unroll
       for (int w = 0; w < G::kw; ++w) {
         uint32_t x[4], y[4];
-        e2m1x8_to_f16x2(kw[t][0][w], x);
-        e2m1x8_to_f16x2(kw[t][1][w], y);
+        e2m1x8_to_f16x2(kw[0][w], x);
+        e2m1x8_to_f16x2(kw[1][w], y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[e] = mul_f16x2(x[e], sc[0][w / 2]);
@@ -466,10 +402,10 @@ struct Decode {
         if (w % wpb == 0)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            f[i] = mx_factor<MODE>((ks[t][i] >> (8 * (w / wpb))) & 255u);
+            f[i] = mx_factor<MODE>((ks[i] >> (8 * (w / wpb))) & 255u);
             f[i] |= f[i] << 16;
           }
-        const uint32_t a = kw[t][0][w], b = kw[t][1][w];
+        const uint32_t a = kw[0][w], b = kw[1][w];
         if constexpr (MODE == kMX4) {
           step_mma(s, 2 * w, mul_bf16x2(e2m1_pair_bf16<0>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<0>(b), f[1]),
                    mul_bf16x2(e2m1_pair_bf16<1>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<1>(b), f[1]));
@@ -496,19 +432,28 @@ struct Decode {
     }
   }
 
-  // O^T += V_hat^T . P^T of tile t; fragment rows g and g + 8 of m-tile mt are
-  // elements (DP / 8) g + 2 mt and the next.
-  __device__ __forceinline__ void weigh(int t, const uint32_t (&ph)[NT][2], const uint32_t (&pl)[NT][2]) {
+  // O^T += V_hat^T . P^T of the tile at token `tok0`; fragment rows g and g + 8
+  // of m-tile mt are elements (DP / 8) g + 2 mt and the next.  Bit i of `in`:
+  // the lane's i-th token counts (what a masked place holds must not: P = 0
+  // does not hide a NaN).
+  __device__ __forceinline__ void weigh(const uint8_t* codes, const uint8_t* scales, uint32_t tok0, uint32_t in, const uint32_t (&ph)[NT][2],
+                                        const uint32_t (&pl)[NT][2]) {
+    uint32_t vw[4][G::vw], vs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      load_value(codes, scales, tok0 + token(2u * c + (i & 1)) + 8u * (i >> 1), vw[i], vs[i]);
+      if (!((in >> i) & 1u)) vs[i] = 0;
+    }
     if constexpr (MODE == kNV) {
 #pragma unroll
       for (int w = 0; w < G::vw; ++w) {
         constexpr int wpb = 2;  // words a block
         const int b = DP == 256 ? w / wpb : 0;
-        const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vs[t][0], vs[t][1], b ? 0x0051 : 0x0040));
-        const uint32_t s23 = e4m3x2_to_f16x2(__byte_perm(vs[t][2], vs[t][3], b ? 0x0051 : 0x0040));
+        const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], b ? 0x0051 : 0x0040));
+        const uint32_t s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], b ? 0x0051 : 0x0040));
         const uint32_t lo = 0x0F0F0F0Fu;
         uint32_t x01[4], y01[4], x23[4], y23[4];
-        const uint32_t v0 = vw[t][0][w], v1 = vw[t][1][w], v2 = vw[t][2][w], v3 = vw[t][3][w];
+        const uint32_t v0 = vw[0][w], v1 = vw[1][w], v2 = vw[2][w], v3 = vw[3][w];
         e2m1x8_to_f16x2((v0 & lo) | ((v1 << 4) & ~lo), x01);
         e2m1x8_to_f16x2(((v0 >> 4) & lo) | (v1 & ~lo), y01);
         e2m1x8_to_f16x2((v2 & lo) | ((v3 << 4) & ~lo), x23);
@@ -519,14 +464,14 @@ struct Decode {
                   mul_f16x2(y23[e], s23), ph, pl);
       }
     } else {
-      const uint32_t f01 = mx_factor<MODE>(vs[t][0]) | (mx_factor<MODE>(vs[t][1]) << 16);
-      const uint32_t f23 = mx_factor<MODE>(vs[t][2]) | (mx_factor<MODE>(vs[t][3]) << 16);
+      const uint32_t f01 = mx_factor<MODE>(vs[0]) | (mx_factor<MODE>(vs[1]) << 16);
+      const uint32_t f23 = mx_factor<MODE>(vs[2]) | (mx_factor<MODE>(vs[3]) << 16);
 #pragma unroll
       for (int w = 0; w < G::vw; ++w)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint32_t sel = hf ? 0x7632u : 0x5410u;
-          const uint32_t u = __byte_perm(vw[t][0][w], vw[t][1][w], sel), v = __byte_perm(vw[t][2][w], vw[t][3][w], sel);
+          const uint32_t u = __byte_perm(vw[0][w], vw[1][w], sel), v = __byte_perm(vw[2][w], vw[3][w], sel);
           if constexpr (MODE == kMX4) {
             out_mma(4 * w + 2 * hf, mul_bf16x2(e2m1_pair_bf16<0>(u), f01), mul_bf16x2(e2m1_pair_bf16<1>(u), f01),
                     mul_bf16x2(e2m1_pair_bf16<0>(v), f23), mul_bf16x2(e2m1_pair_bf16<1>(v), f23), ph, pl);
@@ -541,269 +486,564 @@ struct Decode {
   }
 };
 
-template <typename QT, int MODE, int DP, int NT, bool FAST>
-__global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant__ AttnArgs a) {
-  using D = Decode<QT, MODE, DP, NT, FAST>;
-  constexpr int TS = D::TS, MT = D::G::mtiles, STEP = 16 * TS, ROWS = 8 * NT;
-  __shared__ float sm[kDecWarps][ROWS], sl[kDecWarps][ROWS];
-  __shared__ float so[kDecWarps / 2][ROWS * DP];
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const uint32_t tile = blockIdx.x / a.chunks, chunk = blockIdx.x - tile * a.chunks, hk = blockIdx.y, b = blockIdx.z;
-  const uint32_t r0 = tile * ROWS;
+// A sequence's share of the units: tiles * heads * span of them.
+struct Work {
   Seq s;
-  if (!seq_of(a, b, s)) return;
-  const uint32_t R = s.n * a.G;
-  if (r0 >= R) return;
-  const uint32_t i0 = r0 / a.G, i1 = (min(r0 + ROWS, R) - 1u) / a.G;
-  const Range rg = tile_range(a, s, i0, i1);
-  const int32_t base = rg.lo & ~15;
-  const int32_t span = rg.hi > rg.lo ? rg.hi - base : 0;
-  if (chunk > 0 && (int64_t)chunk * a.chunk >= span) return;
-  const bool whole = span <= a.chunk;
-  const int32_t begin = base + (int32_t)chunk * a.chunk;
-  const int32_t end = min(rg.hi, begin + a.chunk);
-  const Range here{rg.lo, end};
-  const int32_t* table = a.page_table + (uint64_t)b * a.max_pages;
+  int32_t lo, hi, base;  // tokens that any query sees; base: of unit 0
+  uint32_t R, tiles, span;
+};
+template <int ROWS, int UNIT>
+__device__ __forceinline__ bool work_of(const AttnArgs& a, uint32_t b, Work& w) {
+  w.tiles = w.span = 0;
+  if (!seq_of(a, b, w.s) || w.s.n == 0) return false;
+  w.R = w.s.n * a.G;
+  w.tiles = (w.R + ROWS - 1u) / ROWS;
+  w.lo = tile_range(a, w.s, 0, 0).lo;
+  w.hi = tile_range(a, w.s, w.s.n - 1, w.s.n - 1).hi;
+  w.base = w.lo & ~(UNIT - 1);
+  w.span = w.hi > w.lo ? ((uint32_t)(w.hi - w.base) + UNIT - 1u) / UNIT : 1u;  // an empty range is one unit of nothing
+  return true;
+}
 
+// A place in the order of all units.
+template <int ROWS, int UNIT>
+struct Cursor {
+  uint32_t b, tile, hk, off;
+  Work w;
+  // Unit `at` of sequence b.
+  __device__ __forceinline__ void start(const AttnArgs& a, uint32_t b_, uint64_t at) {
+    b = b_;
+    work_of<ROWS, UNIT>(a, b, w);
+    const uint64_t q = at / w.span;
+    off = (uint32_t)(at - q * w.span);
+    tile = (uint32_t)(q / a.heads);
+    hk = (uint32_t)(q - (uint64_t)tile * a.heads);
+  }
+  // The next range's first unit; false past the last sequence.
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    off = 0;
+    if (++hk < a.heads) return true;
+    hk = 0;
+    if (++tile < w.tiles) return true;
+    tile = 0;
+    while (++b < a.B)
+      if (work_of<ROWS, UNIT>(a, b, w)) return true;
+    return false;
+  }
+};
+
+__device__ __forceinline__ uint32_t shared_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(bar)
+               : "memory");
+}
+
+// Waits with a hint of how long (in ns) the thread may be suspended; at most
+// 2^17 * 20 us.
+__device__ __forceinline__ bool wait_for(uint64_t& bar, uint32_t parity) {
+  for (uint32_t i = 0; i < (1u << 17); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(shared_u32(&bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+  }
+  atomicOr(&g_device_error, (unsigned)kDevErrTimeout);
+  return false;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <typename QT, int MODE, int DP, int NT, bool EXACT>
+__global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant__ AttnArgs a) {
+  using D = Decode<QT, MODE, DP, NT, EXACT>;
+  using G = Geo<MODE, DP>;
+  constexpr int TS = D::TS, MT = G::mtiles, ROWS = 8 * NT, UNIT = G::unit, ST = G::stages;
+  extern __shared__ __align__(128) uint8_t stage_mem[];  // ST units: K codes, V codes, K scales, V scales
+  __shared__ __align__(8) uint64_t full[ST], empty[ST];
+  __shared__ uint32_t got[ST][UNIT / 32];                 // a bit for each of the unit's tokens: it is there
+  __shared__ uint64_t wsum[kDecWarps + 1], found_at;
+  __shared__ uint32_t found_b;
+  __shared__ volatile int abort_flag;
+  __shared__ float sm[kDecWarps][ROWS], sl[kDecWarps][ROWS];
+  __shared__ __align__(16) float so[kDecWarps / 2][ROWS * DP];
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const uint32_t rb = a.D * Fmt<MODE>::bits / 8u, sb = a.D / Fmt<MODE>::group;
+  const uint32_t v_at = UNIT * rb, ks_at = 2u * v_at, vs_at = ks_at + UNIT * sb, unit_bytes = 2u * UNIT * (rb + sb);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < ST; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_u32(&full[i])), "r"(1));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_u32(&empty[i])), "r"((int)kDecWarps));
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // All units, then this worker's run [u0, u1) of them and the sequence it
+  // begins in: kDecThreads sequences at a time.
+  auto units_of = [&](uint32_t b) -> uint64_t {
+    Work w;
+    return b < a.B && work_of<ROWS, UNIT>(a, b, w) ? (uint64_t)w.tiles * a.heads * w.span : 0;
+  };
+  const uint64_t mine = units_of(threadIdx.x);
+  uint64_t total = mine;
+  for (uint32_t b = threadIdx.x + kDecThreads; b < a.B; b += kDecThreads) total += units_of(b);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  if (lane == 0) wsum[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w <= kDecWarps; ++w) total += wsum[w];
+  const uint32_t workers = (uint32_t)min((uint64_t)gridDim.x, total);
+  if (blockIdx.x >= workers) {
+    if (a.split && threadIdx.x == 0) a.part_head[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  const uint64_t u0 = total * blockIdx.x / workers, u1 = total * (blockIdx.x + 1) / workers;
+  uint64_t before = 0;  // units of the sequences before this round's
+  if (threadIdx.x == 0) found_b = a.B;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += kDecThreads) {
+    const uint64_t v = b0 ? units_of(b0 + threadIdx.x) : mine;
+    uint64_t incl = v;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= (uint32_t)x) incl += y;
+    }
+    __syncthreads();  // wsum is read
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    uint64_t round = 0;
+#pragma unroll
+    for (int w = 0; w <= kDecWarps; ++w) {
+      if ((uint32_t)w < warp) incl += wsum[w];
+      round += wsum[w];
+    }
+    if (u0 < before + round) {
+      incl += before;
+      if (u0 < incl && u0 >= incl - v) {
+        found_b = b0 + threadIdx.x;
+        found_at = incl - v;
+      }
+      break;
+    }
+    before += round;
+  }
+  __syncthreads();
+  if (found_b >= a.B) return;  // the lengths changed meanwhile
+
+  Cursor<ROWS, UNIT> at;
+  at.start(a, found_b, u0 - found_at);
+  uint64_t u = u0;
+  bool more = true;
+  if (!a.split && at.off) {  // without partial results a range belongs to the worker it begins in
+    u += at.w.span - at.off;
+    more = u < u1 && at.next(a);
+  }
+  // units of the current range that this worker takes
+  auto take = [&]() { return a.split ? (uint32_t)min((uint64_t)(at.w.span - at.off), u1 - u) : at.w.span; };
+
+  if (warp == kDecWarps) {
+    // ------------------------------------------------------------ copies
+    // run: tokens that lie together on one page whatever unit they are in
+    const uint32_t run = min((uint32_t)UNIT, a.page_size & (0u - a.page_size));
+    uint32_t it = 0;
+    bool ok = true;
+    int64_t row = -1;  // of this lane's run in the unit to come, looked up a unit ahead
+    while (more && ok) {
+      const uint32_t n = take();
+      const int32_t* table = a.page_table + (uint64_t)at.b * a.max_pages;
+      auto row_of = [&](int32_t j) -> int64_t {
+        const uint32_t pg = a.by_page.div((uint32_t)j);
+        const int32_t page = __ldg(table + pg);
+        if ((uint32_t)page < a.num_pages)
+          return (int64_t)(((uint64_t)(uint32_t)page * a.heads + at.hk) * a.page_size + ((uint32_t)j - pg * a.page_size));
+        atomicOr(&g_device_error, (unsigned)kDevErrIndex);
+        return -1;
+      };
+      const uint32_t part = lane & 3u, r = lane >> 2;
+      auto look = [&](uint32_t k) {  // 16-token pieces at least: lane = run * 4 + part
+        const int32_t j = at.w.base + (int32_t)((at.off + k) * UNIT + r * run);
+        row = run >= 16u && r * run < (uint32_t)UNIT && j < at.w.hi && j + (int32_t)run > at.w.lo ? row_of(j) : -1;
+      };
+      if (n > 0) look(0);
+      for (uint32_t k = 0; k < n; ++k, ++it) {
+        const uint32_t st = it % ST;
+        if (!__all_sync(0xffffffffu, wait_for(empty[st], (it / ST & 1u) ^ 1u) && !abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int32_t t0 = at.w.base + (int32_t)((at.off + k) * UNIT);
+        const uint32_t bar = shared_u32(&full[st]), dst = shared_u32(stage_mem) + st * unit_bytes;
+        if (run >= 16u) {
+          const int32_t j = t0 + (int32_t)(r * run);
+          const uint32_t cnt = row >= 0 ? min(run, ((uint32_t)(at.w.hi - j) + 15u) & ~15u) : 0u;
+          uint32_t tokens = 0;
+#pragma unroll
+          for (int i = 0; i < UNIT / 32; ++i) {
+            const int from = max((int)(r * run) - 32 * i, 0), to = min((int)(r * run + cnt) - 32 * i, 32);
+            const uint32_t mask = __reduce_or_sync(0xffffffffu, to > from ? (0xffffffffu >> (32 - to)) & (0xffffffffu << from) : 0u);
+            if (lane == 0) got[st][i] = mask;
+            tokens += __popc(mask);
+          }
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(tokens * 2u * (rb + sb)) : "memory");
+          __syncwarp();
+          if (cnt) {
+            const uint32_t bytes = part < 2u ? rb : sb;
+            const uint8_t* src = part == 0 ? a.codes[0] : part == 1 ? a.codes[1] : part == 2 ? a.scales[0] : a.scales[1];
+            bulk_copy(dst + (part == 0 ? 0u : part == 1 ? v_at : part == 2 ? ks_at : vs_at) + r * run * bytes, src + (uint64_t)row * bytes,
+                      cnt * bytes, bar);
+          }
+          if (k + 1 < n) look(k + 1);
+        } else {
+          // pages that end inside a 16-token piece: token by token, scales by
+          // plain loads (their rows need not be 16 bytes long)
+          int64_t y[UNIT / 32];
+          uint32_t tokens = 0;
+#pragma unroll
+          for (int i = 0; i < UNIT / 32; ++i) {
+            const uint32_t x = 32u * i + lane;
+            const int32_t j = t0 + (int32_t)x;
+            y[i] = j >= at.w.lo && j < at.w.hi ? row_of(j) : -1;
+            const uint32_t mask = __ballot_sync(0xffffffffu, y[i] >= 0);
+            if (lane == 0) got[st][i] = mask;
+            tokens += __popc(mask);
+            uint8_t* sc = stage_mem + st * unit_bytes + ks_at + x * sb;
+            for (uint32_t e = 0; y[i] >= 0 && e < sb; ++e) {
+              sc[e] = __ldg(a.scales[0] + (uint64_t)y[i] * sb + e);
+              sc[UNIT * sb + e] = __ldg(a.scales[1] + (uint64_t)y[i] * sb + e);
+            }
+          }
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(tokens * 2u * rb) : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < UNIT / 32; ++i) {
+            const uint32_t x = 32u * i + lane;
+            if (y[i] >= 0) {
+              bulk_copy(dst + x * rb, a.codes[0] + (uint64_t)y[i] * rb, rb, bar);
+              bulk_copy(dst + v_at + x * rb, a.codes[1] + (uint64_t)y[i] * rb, rb, bar);
+            }
+          }
+        }
+      }
+      u += n;
+      more = ok && u < u1 && at.next(a);
+    }
+    if (!ok && lane == 0) abort_flag = 1;
+    // what was asked for has landed before the CTA's memory goes
+    for (uint32_t i = it > (uint32_t)ST ? it - ST : 0; i < it; ++i) wait_for(full[i % ST], i / ST & 1u);
+    return;
+  }
+
+  // -------------------------------------------------------------- the rest
   D d;
   d.lane = lane;
   d.g = lane >> 2;
   d.c = lane & 3u;
-  d.load_q(a, s, hk, r0, R);
-  // what this lane's columns (rows r0 + 8 nt + 2c, + 1) see
-  int32_t see_lo[NT][2], see_hi[NT][2];
-  int32_t all_lo = rg.lo, all_hi = end;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t i = min(r0 + 8u * nt + 2u * d.c + e, R - 1u) / a.G;
-      const Range r = tile_range(a, s, i, i);
-      see_lo[nt][e] = r.lo;
-      see_hi[nt][e] = r.hi;
-      d.m[nt][e] = -INFINITY;
-      d.l[nt][e] = 0.0f;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) d.o[nt][mt][2 * e] = d.o[nt][mt][2 * e + 1] = 0.0f;
-    }
-  // tokens every row of the tile sees
-  if (a.window) all_lo = tile_range(a, s, i1, i1).lo;
-  if (a.causal) all_hi = min(end, tile_range(a, s, i0, i0).hi);
-
-  // The loads of the next step are issued as soon as this one's registers are
-  // free: keys after the logits, values after the weighted sum; the page
-  // numbers a step earlier still.
-  int32_t j0 = begin + (int32_t)warp * STEP;
-  int32_t pages[TS];
-  auto look = [&](int32_t j) {
-#pragma unroll
-    for (int t = 0; t < TS; ++t) pages[t] = FAST && j + 16 * t < end ? __ldg(table + a.by_page.div((uint32_t)(j + 16 * t))) : -1;
-  };
-  uint32_t rows[TS];
-  bool inside = false;
-  auto find = [&](int32_t j) {
-    inside = FAST && j >= rg.lo && j + STEP <= end;
-#pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      inside = inside && (uint32_t)pages[t] < a.num_pages;
-      rows[t] = d.tile_row(a, pages[t], hk, j + 16 * t);
-    }
-  };
-  uint32_t there = 0;
-  if (j0 < end) {
-    look(j0);
-    find(j0);
-    look(j0 + kDecWarps * STEP);
-    there = d.load_keys(a, table, hk, j0, here, inside, rows);
-    d.load_values(a, table, hk, j0, here, inside, rows);
-  }
-  for (; j0 < end; j0 += kDecWarps * STEP) {
-    const int32_t jn = j0 + kDecWarps * STEP;
-    const uint32_t now = there;
-    float sv[TS][NT][4];
-#pragma unroll
-    for (int t = 0; t < TS; ++t) d.logits(t, sv[t]);
-    if (jn < end) {
-      find(jn);
-      look(jn + kDecWarps * STEP);
-      there = d.load_keys(a, table, hk, jn, here, inside, rows);
-    }
-    const bool full = __all_sync(0xffffffffu, now == (1u << (2 * TS)) - 1u) && j0 >= all_lo && j0 + STEP <= all_hi;
-    if (!full) {
-#pragma unroll
-      for (int t = 0; t < TS; ++t)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int32_t j = j0 + 16 * t + 8 * (e >> 1) + d.g;
-            if (!((now >> (2 * t + (e >> 1))) & 1u) || j < see_lo[nt][e & 1] || j >= see_hi[nt][e & 1]) sv[t][nt][e] = -INFINITY;
-          }
-    }
-    // The running maximum moves only when a step exceeds it by 2^8 (weights
-    // then lie below 2^8, which fp16 and the sums hold as well as below 1).
-    float top[NT][2];
-    bool grow = false;
+  d.rb = rb;
+  d.sb = sb;
+  d.D = a.D;
+  if (a.split && threadIdx.x == 0) a.part_head[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  uint32_t it = 0;
+  for (uint32_t seg = 0; more; ++seg) {
+    const uint32_t n = take(), r0 = at.tile * ROWS, R = at.w.R;
+    const Seq s = at.w.s;
+    const bool whole = at.off == 0 && n == at.w.span;
+    d.load_q(a, s, at.hk, r0, R);
+    // what this lane's columns (rows r0 + 8 nt + 2c, + 1) see
+    int32_t see_lo[NT][2], see_hi[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = -INFINITY;
+        const uint32_t i = min(r0 + 8u * nt + 2u * d.c + e, R - 1u) / a.G;
+        const Range r = tile_range(a, s, i, i);
+        see_lo[nt][e] = r.lo;
+        see_hi[nt][e] = r.hi;
+        d.m[nt][e] = -INFINITY;
+        d.l[nt][e] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < TS; ++t) x = fmaxf(x, fmaxf(sv[t][nt][e], sv[t][nt][2 + e]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        top[nt][e] = x * d.fz[nt][e] - (D::kMx ? 32.0f : 0.0f);
-        grow = grow || top[nt][e] > d.m[nt][e] + 8.0f;
+        for (int mt = 0; mt < MT; ++mt) d.o[nt][mt][2 * e] = d.o[nt][mt][2 * e + 1] = 0.0f;
       }
-    if (__any_sync(0xffffffffu, grow)) {
+    // tokens every row of the tile sees
+    const uint32_t i0 = r0 / a.G, i1 = (min(r0 + ROWS, R) - 1u) / a.G;
+    const int32_t all_lo = max(at.w.lo, tile_range(a, s, i1, i1).lo), all_hi = min(at.w.hi, tile_range(a, s, i0, i0).hi);
+
+    for (uint32_t k = 0; k < n; ++k, ++it) {
+      const uint32_t st = it % ST;
+      // once a wait has run out nothing is waited for: the sums are void, the host is told
+      if (!__any_sync(0xffffffffu, abort_flag) && !__all_sync(0xffffffffu, wait_for(full[st], it / ST & 1u))) abort_flag = 1;
+      const uint8_t* mem = stage_mem + st * unit_bytes;
+      const uint32_t tok0 = warp * 16u * TS;
+      const int32_t j0 = at.w.base + (int32_t)((at.off + k) * UNIT + tok0);
+      const uint32_t there = TS == 2 ? got[st][warp] : got[st][warp >> 1] >> (16u * (warp & 1u)) & 0xffffu;
+      const bool full_step = there == (TS == 2 ? 0xffffffffu : 0xffffu) && j0 >= all_lo && j0 + 16 * TS <= all_hi;
+      float sv[TS][NT][4];
+#pragma unroll
+      for (int t = 0; t < TS; ++t) d.logits(mem, mem + ks_at, tok0 + 16u * t, sv[t]);
+      uint32_t in[TS];  // weigh's tokens that count
+#pragma unroll
+      for (int t = 0; t < TS; ++t) in[t] = 15u;
+      if (!full_step) {
+#pragma unroll
+        for (int t = 0; t < TS; ++t) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = 16u * t + 8u * (e >> 1) + D::token(d.g);
+              const int32_t j = j0 + (int32_t)x;
+              if (!((there >> x) & 1u) || j < see_lo[nt][e & 1] || j >= see_hi[nt][e & 1]) sv[t][nt][e] = -INFINITY;
+            }
+          in[t] = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = 16u * t + 8u * (i >> 1) + D::token(2u * d.c + (i & 1));
+            const int32_t j = j0 + (int32_t)x;
+            in[t] |= ((there >> x) & 1u) && j >= at.w.lo && j < at.w.hi ? 1u << i : 0u;
+          }
+        }
+      }
+      // The running maximum moves only when a step exceeds it by 2^8 (weights
+      // then lie below 2^8, which fp16 and the sums hold as well as below 1).
+      float top[NT][2];
+      bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(d.m[nt][e], top[nt][e]);
-          const float f = mn == -INFINITY ? 1.0f : ex2(d.m[nt][e] - mn);
-          d.m[nt][e] = mn;
-          d.l[nt][e] *= f;
+          float x = -INFINITY;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            d.o[nt][mt][e] *= f;
-            d.o[nt][mt][2 + e] *= f;
+          for (int t = 0; t < TS; ++t) x = fmaxf(x, fmaxf(sv[t][nt][e], sv[t][nt][2 + e]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          top[nt][e] = x * d.fz[nt][e] - (D::kMx ? 32.0f : 0.0f);
+          grow = grow || top[nt][e] > d.m[nt][e] + 8.0f;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(d.m[nt][e], top[nt][e]);
+            const float f = mn == -INFINITY ? 1.0f : ex2(d.m[nt][e] - mn);
+            d.m[nt][e] = mn;
+            d.l[nt][e] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              d.o[nt][mt][e] *= f;
+              d.o[nt][mt][2 + e] *= f;
+            }
+          }
+      }
+      float ref[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[nt][e] = d.m[nt][e] == -INFINITY ? 0.0f : d.m[nt][e];
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(fmaf(sv[t][nt][e], d.fz[nt][e & 1], -ref[nt][e & 1]));
+            d.l[nt][e & 1] += p[e];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (!D::kMx) {
+              ph[nt][i] = transpose8x8(pack_f16x2(p[2 * i], p[2 * i + 1]));
+            } else {
+              const uint32_t hi = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+              const uint32_t lo = pack_bf16x2(p[2 * i] - __uint_as_float(hi << 16), p[2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u));
+              ph[nt][i] = transpose8x8(hi);
+              pl[nt][i] = transpose8x8(lo);
+            }
           }
         }
+        d.weigh(mem + v_at, mem + vs_at, tok0 + 16u * t, in[t], ph, pl);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(shared_u32(&empty[st]));
     }
-    float ref[NT][2];
+
+    // Join the warps: a common maximum first, then the sums, two warps at a time.
+    auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[nt][e] = d.m[nt][e] == -INFINITY ? 0.0f : d.m[nt][e];
-#pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(fmaf(sv[t][nt][e], d.fz[nt][e & 1], -ref[nt][e & 1]));
-          d.l[nt][e & 1] += p[e];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if constexpr (!D::kMx) {
-            ph[nt][i] = transpose8x8(pack_f16x2(p[2 * i], p[2 * i + 1]));
-          } else {
-            const uint32_t hi = pack_bf16x2(p[2 * i], p[2 * i + 1]);
-            const uint32_t lo = pack_bf16x2(p[2 * i] - __uint_as_float(hi << 16), p[2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u));
-            ph[nt][i] = transpose8x8(hi);
-            pl[nt][i] = transpose8x8(lo);
-          }
-        }
+      for (int e = 0; e < 2; ++e) {
+        float& l = d.l[nt][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (d.g == 0) sm[warp][8 * nt + 2 * d.c + e] = d.m[nt][e];
       }
-      d.weigh(t, ph, pl);
-    }
-    if (jn < end) d.load_values(a, table, hk, jn, here, inside, rows);
-  }
-
-  // Join the warps: a common maximum first, then the sums, two warps at a time.
+    sync();
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float& l = d.l[nt][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (d.g == 0) sm[warp][8 * nt + 2 * d.c + e] = d.m[nt][e];
-    }
-  __syncthreads();
+      for (int e = 0; e < 2; ++e) {
+        float M = -INFINITY;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, sm[w][8 * nt + 2 * d.c + e]);
-      const float f = d.m[nt][e] == -INFINITY ? 0.0f : ex2(d.m[nt][e] - M);
-      d.m[nt][e] = M;
-      d.l[nt][e] *= f;
-      if (d.g == 0) sl[warp][8 * nt + 2 * d.c + e] = d.l[nt][e];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        d.o[nt][mt][e] *= f;
-        d.o[nt][mt][2 + e] *= f;
-      }
-    }
-#pragma unroll
-  for (int half = kDecWarps / 2; half > 0; half >>= 1) {
-    if (warp >= (uint32_t)half && warp < 2u * half) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          reinterpret_cast<float4*>(so[warp - half])[(nt * MT + mt) * 32 + lane] =
-              make_float4(d.o[nt][mt][0], d.o[nt][mt][1], d.o[nt][mt][2], d.o[nt][mt][3]);
-    }
-    __syncthreads();
-    if (warp < (uint32_t)half) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, sm[w][8 * nt + 2 * d.c + e]);
+        const float f = d.m[nt][e] == -INFINITY ? 0.0f : ex2(d.m[nt][e] - M);
+        d.m[nt][e] = M;
+        d.l[nt][e] *= f;
+        if (d.g == 0) sl[warp][8 * nt + 2 * d.c + e] = d.l[nt][e];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float4 v = reinterpret_cast<const float4*>(so[warp])[(nt * MT + mt) * 32 + lane];
-          d.o[nt][mt][0] += v.x;
-          d.o[nt][mt][1] += v.y;
-          d.o[nt][mt][2] += v.z;
-          d.o[nt][mt][3] += v.w;
+          d.o[nt][mt][e] *= f;
+          d.o[nt][mt][2 + e] *= f;
         }
+      }
+#pragma unroll
+    for (int half = kDecWarps / 2; half > 0; half >>= 1) {
+      if (warp >= (uint32_t)half && warp < 2u * half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            reinterpret_cast<float4*>(so[warp - half])[(nt * MT + mt) * 32 + lane] =
+                make_float4(d.o[nt][mt][0], d.o[nt][mt][1], d.o[nt][mt][2], d.o[nt][mt][3]);
+      }
+      sync();
+      if (warp < (uint32_t)half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float4 v = reinterpret_cast<const float4*>(so[warp])[(nt * MT + mt) * 32 + lane];
+            d.o[nt][mt][0] += v.x;
+            d.o[nt][mt][1] += v.y;
+            d.o[nt][mt][2] += v.z;
+            d.o[nt][mt][3] += v.w;
+          }
+      }
+      sync();
     }
-    __syncthreads();
+    if (warp == 0) {
+      const uint32_t slot = 2u * blockIdx.x + (seg ? 1u : 0u);
+      const float fv = D::kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t lr = 8u * nt + 2u * d.c + e, r = r0 + lr;
+          if (r >= R) continue;
+          float l = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) l += sl[w][lr];
+          const uint32_t i = r / a.G, h = at.hk * a.G + (r - i * a.G);
+          const uint64_t to = (uint64_t)(s.t0 + i) * a.Hq + h;
+          const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
+          if (whole) {
+            if (a.lse && d.g == 0) a.lse[to] = l > 0.0f ? (d.m[nt][e] + log2f(l)) * kLn2 : -INFINITY;
+          } else if (d.g == 0) {
+            a.part_ml[slot * ROWS + lr] = make_float2(d.m[nt][e], l);
+          }
+#pragma unroll
+          for (int k = 0; k < DP / 64; ++k) {  // eight elements: m-tiles 4k .. 4k + 3
+            const uint32_t el = d.g * (DP / 8) + 8u * k;
+            if (el >= a.D) continue;
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              v[2 * x] = d.o[nt][4 * k + x][e] * f;
+              v[2 * x + 1] = d.o[nt][4 * k + x][2 + e] * f;
+            }
+            if (whole)
+              store8<QT>(static_cast<QT*>(a.out) + to * a.D + el, v);
+            else
+              store8<float>(a.part_o + ((uint64_t)slot * ROWS + lr) * a.D + el, v);
+          }
+        }
+      // The worker that begins a range it does not end says which workers have
+      // the rest: the next ones, each in its first slot.
+      if (!whole && at.off == 0 && lane == 0) {
+        const uint64_t last = u + at.w.span - 1u;  // the range's last unit
+        const uint32_t worker = (uint32_t)(((last + 1u) * workers - 1u) / total);
+        a.part_head[2 * blockIdx.x] = make_int4((int)worker + 1, (int)slot, (int)(s.t0 + r0 / a.G), (int)min((uint32_t)ROWS, R - r0));
+        a.part_head[2 * blockIdx.x + 1] = make_int4((int)(r0 % a.G), (int)at.hk, 0, 0);
+      }
+    }
+    u += n;
+    more = u < u1 && at.next(a);
   }
-  if (warp != 0) return;
-  const float fv = D::kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t r = r0 + 8u * nt + 2u * d.c + e;
-      if (r >= R) continue;
-      float l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) l += sl[w][8 * nt + 2 * d.c + e];
-      const uint32_t i = r / a.G, h = hk * a.G + (r - i * a.G);
-      const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
-      const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
-      if (whole) {
-        if (a.lse && d.g == 0) a.lse[at] = l > 0.0f ? (d.m[nt][e] + log2f(l)) * kLn2 : -INFINITY;
-      } else if (d.g == 0) {
-        a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(d.m[nt][e], l);
-      }
-#pragma unroll
-      for (int k = 0; k < DP / 64; ++k) {  // eight elements: m-tiles 4k .. 4k + 3
-        const uint32_t el = d.g * (DP / 8) + 8u * k;
-        if (el >= a.D) continue;
-        float v[8];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          v[2 * x] = d.o[nt][4 * k + x][e] * f;
-          v[2 * x + 1] = d.o[nt][4 * k + x][2 + e] * f;
-        }
-        if (whole)
-          store8<QT>(static_cast<QT*>(a.out) + at * a.D + el, v);
-        else
-          store8<float>(a.part_o + ((uint64_t)chunk * a.T * a.Hq + at) * a.D + el, v);
-      }
-    }
 }
 
-// Join of the partial results of one (query, head): one CTA, a warp for every
+// Join of one row (blockIdx.y) of the range that worker blockIdx.x began and
+// others went on with: a warp for every fourth part, the row's elements over
+// the lanes.
+template <typename QT, int ROWS>
+__global__ void __launch_bounds__(128) k_kv_decode_join(const __grid_constant__ AttnArgs a) {
+  __shared__ float sl[4];
+  __shared__ __align__(16) float so[4][256];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 head = a.part_head[2 * blockIdx.x], more = a.part_head[2 * blockIdx.x + 1];
+  const uint32_t lr = blockIdx.y;
+  if (head.x == 0 || lr >= (uint32_t)head.w) return;
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const uint32_t parts = (uint32_t)head.x - blockIdx.x, d0 = lane * 8u;
+  auto slot = [&](uint32_t k) { return k == 0 ? (uint32_t)head.y : 2u * (blockIdx.x + k); };
+  float m = -INFINITY;
+  for (uint32_t k = lane; k < parts; k += 32) m = fmaxf(m, a.part_ml[slot(k) * ROWS + lr].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float l = 0.0f, o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll 4
+  for (uint32_t k = warp; k < parts; k += 4) {
+    const float2 ml = a.part_ml[slot(k) * ROWS + lr];
+    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+    l += ml.y * f;
+    if (d0 < a.D) {
+      float v[8];
+      load8_shared<float>(a.part_o + ((uint64_t)slot(k) * ROWS + lr) * a.D + d0, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e], f, o[e]);
+    }
+  }
+  if (lane == 0) sl[warp] = l;
+  if (d0 < a.D) store8<float>(&so[warp][d0], o);
+  __syncthreads();
+  if (warp != 0) return;
+  l = sl[0] + sl[1] + sl[2] + sl[3];
+  const uint32_t x = (uint32_t)more.x + lr, i = x / a.G;  // query after the tile's first, head of the group
+  const uint64_t at = (uint64_t)((uint32_t)head.z + i) * a.Hq + (uint32_t)more.y * a.G + (x - i * a.G);
+  if (a.lse && lane == 0) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (d0 >= a.D) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = so[0][d0 + e] + so[1][d0 + e] + so[2][d0 + e] + so[3][d0 + e];
+    v[e] = l > 0.0f ? v[e] / l : 0.0f;
+  }
+  store8<QT>(static_cast<QT*>(a.out) + at * a.D + d0, v);
+}
+
+// k_kv_prefill's join.  One (query, head): one CTA, a warp for every
 // fourth chunk, the row's elements over the lanes.
 constexpr int kJoinWarps = 4;
 template <typename QT>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_constant__ AttnArgs a) {
   __shared__ float sl[kJoinWarps];
-  __shared__ float so[kJoinWarps][256];
+  __shared__ __align__(16) float so[kJoinWarps][256];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   Seq s;

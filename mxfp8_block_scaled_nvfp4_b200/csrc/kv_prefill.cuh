@@ -84,27 +84,6 @@ __device__ __forceinline__ void st_shared_u8(uint32_t at, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// tc::mbar_wait with a hint of how long (in ns) the thread may be suspended: a
-// warp that polls takes issue slots from the ones it waits for.  At most
-// 2^17 * 20 us.
-__device__ __forceinline__ bool wait_for(uint64_t& bar, uint32_t parity) {
-  for (uint32_t i = 0; i < (1u << 17); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(&bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-  }
-  atomicOr(&g_device_error, (unsigned)kDevErrTimeout);
-  return false;
-}
-__device__ __forceinline__ void arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"

@@ -922,31 +922,39 @@ nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
   return check_launch(tag);
 }
 
-// How kv_attention cuts its work: the kernel, rows of queries a CTA holds,
-// tokens a CTA walks and the largest number of such chunks a row tile can have.
+// How kv_attention cuts its work.  k_kv_prefill: rows of queries a CTA holds,
+// tokens a CTA walks and the largest number of such chunks a row tile can
+// have.  k_kv_decode: rows of a tile; its CTAs share out the rest themselves.
 struct KvPlan {
   bool prefill;
-  int64_t tile_rows, chunk, chunks, bytes_per_chunk;
+  int64_t tile_rows, chunk, chunks;
+  size_t bytes_per_chunk;  // k_kv_decode: of partial results per worker
 };
+constexpr int64_t kKvMaxWorkers = 148 * 4, kKvWorkers = 148;  // most, and fewest worth splitting over
 static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
                       int64_t window, bool prefill_has_it, size_t workspace_bytes) {
   KvPlan p;
   const int64_t rows = max_q * (Hq / heads);
   p.prefill = prefill_has_it && rows > 32;
-  p.tile_rows = p.prefill ? (D > 128 ? 128 : 256) : rows <= 8 || D > 128 ? 8 : 16;
-  p.bytes_per_chunk = T * Hq * (D * 4 + 8);
+  p.chunk = p.chunks = 1;
+  if (!p.prefill) {
+    p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;
+    p.bytes_per_chunk = (size_t)(2 * p.tile_rows * (D * 4 + 8) + 32);
+    return p;
+  }
+  p.tile_rows = D > 128 ? 128 : 256;
+  p.bytes_per_chunk = (size_t)(T * Hq * (D * 4 + 8));
   // tokens a tile's range can span, from a multiple of 16
   int64_t span = max_kv;
   if (window > 0 && window + max_q + 30 < span) span = window + max_q + 30;
   const double tiles = (double)B * (double)heads * (double)((rows + p.tile_rows - 1) / p.tile_rows);
-  const int64_t least = p.prefill ? 512 : 128;
-  const double share = (double)span * tiles / (p.prefill ? 148 : 148 * 6);  // may exceed 64-bit integers
+  const double share = (double)span * tiles / 148;  // may exceed 64-bit integers
   int64_t chunk = share < (double)span ? (int64_t)share + 1 : span;
-  int64_t fit = workspace_bytes == SIZE_MAX ? span : (int64_t)(workspace_bytes / (size_t)p.bytes_per_chunk);
+  int64_t fit = workspace_bytes == SIZE_MAX ? span : (int64_t)(workspace_bytes / p.bytes_per_chunk);
   if (fit < 2) fit = 1;
   if ((span + fit - 1) / fit > chunk) chunk = (span + fit - 1) / fit;
   p.chunk = (chunk + 127) / 128 * 128;
-  if (p.chunk < least) p.chunk = least;
+  if (p.chunk < 512) p.chunk = 512;
   p.chunks = span > 0 ? (span + p.chunk - 1) / p.chunk : 1;
   return p;
 }
@@ -960,7 +968,9 @@ size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t hea
   size_t most = 0;  // over the kernels that the types may choose
   for (int i = 0; i < 2; ++i) {
     const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, SIZE_MAX);
-    const size_t bytes = p.chunks > 1 ? (size_t)(p.chunks * p.bytes_per_chunk) : 0;
+    // 64 tokens are one unit of work: nothing to split
+    const size_t bytes = p.prefill ? (p.chunks > 1 ? p.chunks * p.bytes_per_chunk : 0)
+                                   : (max_kv > 64 ? (size_t)kKvMaxWorkers * p.bytes_per_chunk : 0);
     if (bytes > most) most = bytes;
   }
   return most;
@@ -1044,43 +1054,76 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.chunk = (int32_t)p.chunk;
   a.chunks = (uint32_t)p.chunks;
   a.tile_rows = (uint32_t)p.tile_rows;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (size_t)p.chunks * T * Hq * cache->D * 4);
   const int64_t tiles = (max_q * a.G + p.tile_rows - 1) / p.tile_rows;
-  if (product_exceeds(tiles, p.chunks, INT32_MAX)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q and max_kv too large", tag);
-  if (p.prefill && product_exceeds(tiles * p.chunks, B * cache->heads, INT32_MAX))
-    return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q, max_kv and B too large together", tag);
-  const dim3 grid = p.prefill ? dim3((unsigned)(tiles * p.chunks * B * cache->heads)) : dim3((unsigned)(tiles * p.chunks), a.heads, a.B);
-  const bool one_page = a.page_size % 16 == 0 && !product_exceeds(cache->num_pages * cache->page_size, cache->heads, UINT32_MAX);
+  int64_t workers = 0;  // the most that there is workspace for
+  if (p.prefill) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (size_t)p.chunks * T * Hq * cache->D * 4);
+    if (product_exceeds(tiles, p.chunks, INT32_MAX) || product_exceeds(tiles * p.chunks, B * cache->heads, INT32_MAX))
+      return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q, max_kv and B too large together", tag);
+  } else {
+    workers = (int64_t)(workspace_bytes / p.bytes_per_chunk);
+    if (workers > kKvMaxWorkers) workers = kKvMaxWorkers;
+    a.split = workers >= kKvWorkers && max_kv > 64;
+    if (!a.split) workers = kKvMaxWorkers;
+    a.part_head = static_cast<int4*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (size_t)workers * 32);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)workers * 2 * p.tile_rows * cache->D);
+  }
   cudaError_t e = cudaSuccess;
   dispatch_mode(cache->mode, [&](auto m) {
     constexpr int MODE = decltype(m)::value;
     auto with_type = [&](auto t) {
       using QT = decltype(t);
+      // k_kv_decode over row tiles of ROWS
+      auto decode = [&](auto kern, auto rows_tag, int smem) {
+        constexpr int ROWS = decltype(rows_tag)::value;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return;
+        int64_t grid = (int64_t)d.sm_count * resident_ctas((const void*)kern, kv::kDecThreads, (size_t)smem);
+        if (grid > workers) grid = workers;
+        kern<<<(unsigned)grid, kv::kDecThreads, smem, stream>>>(a);
+        if (!a.split) return;
+        // the join's launch overlaps the kernel before it
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3((unsigned)grid, ROWS);
+        cfg.blockDim = dim3(128);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv::k_kv_decode_join<QT, ROWS>, a);
+      };
       auto with_dim = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
         if (p.prefill) {
           if constexpr (MODE == kv::kNV || std::is_same<QT, __nv_bfloat16>::value) {
             auto kern = kv::pf::k_kv_prefill<QT, MODE, DP>;
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv::pf::Shape<MODE, DP>::smem);
-            if (e == cudaSuccess) kern<<<grid, kv::pf::THREADS, kv::pf::Shape<MODE, DP>::smem, stream>>>(a);
+            if (e != cudaSuccess) return;
+            kern<<<(unsigned)(tiles * p.chunks * B * cache->heads), kv::pf::THREADS, kv::pf::Shape<MODE, DP>::smem, stream>>>(a);
+            if (p.chunks > 1) kv::k_kv_join<QT><<<dim3(a.max_q, a.Hq, a.B), kv::kJoinWarps * 32, 0, stream>>>(a);
           }
           return;
         }
-        auto go = [&](auto kern) { kern<<<grid, kv::kDecThreads, 0, stream>>>(a); };
-        const bool fast = one_page && a.D == (uint32_t)DP;
+        const bool exact = a.D == (uint32_t)DP;
+        constexpr int smem = kv::Geo<MODE, DP>::stages * kv::Geo<MODE, DP>::unit_bytes;
         if constexpr (DP <= 128) {
           if (p.tile_rows == 16) {
-            fast ? go(kv::k_kv_decode<QT, MODE, DP, 2, true>) : go(kv::k_kv_decode<QT, MODE, DP, 2, false>);
+            const std::integral_constant<int, 16> r;
+            exact ? decode(kv::k_kv_decode<QT, MODE, DP, 2, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 2, false>, r, smem);
             return;
           }
         }
-        fast ? go(kv::k_kv_decode<QT, MODE, DP, 1, true>) : go(kv::k_kv_decode<QT, MODE, DP, 1, false>);
+        const std::integral_constant<int, 8> r;
+        exact ? decode(kv::k_kv_decode<QT, MODE, DP, 1, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 1, false>, r, smem);
       };
       if (a.D <= 64) with_dim(std::integral_constant<int, 64>{});
       else if (a.D <= 128) with_dim(std::integral_constant<int, 128>{});
       else with_dim(std::integral_constant<int, 256>{});
-      if (e == cudaSuccess && p.chunks > 1) kv::k_kv_join<QT><<<dim3(a.max_q, a.Hq, a.B), kv::kJoinWarps * 32, 0, stream>>>(a);
     };
     if (q_dt == NVFP4_DT_F16) with_type(__half{});
     else with_type(__nv_bfloat16{});
