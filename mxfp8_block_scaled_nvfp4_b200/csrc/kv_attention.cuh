@@ -106,10 +106,9 @@ __device__ __forceinline__ float ex2(float x) {
 // 131072 tokens took 55 us in 2.4 waves, 47 us in one).  A run begins and
 // ends anywhere in a range: what it does not cover whole goes to k_kv_join.
 //
-// In a CTA a fifth warp copies the units ahead into shared memory with bulk
-// copies (one a page, or a 16-token piece of one, and part: K and V codes, K
-// and V scales), so loads cost the other four neither instructions nor
-// registers; each of those takes 16 * TS tokens of every unit, with its own
+// In a CTA a fifth warp copies the units ahead into shared memory, so loads
+// cost the other four neither instructions nor registers: one bulk copy a page
+// (or piece of one) and part (K and V codes, K and V scales); each of those takes 16 * TS tokens of every unit, with its own
 // running maximum, and they join at the end of a range.  Codes go from shared
 // memory straight into matrix fragments: a quad of lanes holds one token's
 // key row (the order of the elements along D is free as long as q's fragments
@@ -260,8 +259,7 @@ struct Decode {
     return MODE == kNV ? 4 * s + 2 * j + e : MODE == kMX4 ? 8 * (s / 2) + 2 * (s % 2) + j + 4 * e : 4 * s + j + 2 * e;
   }
 
-  __device__ __forceinline__ void load_q(const AttnArgs& a, const Seq& sq, uint32_t hk, uint32_t r0, uint32_t R) {
-    const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
+  __device__ __forceinline__ void load_q(const AttnArgs& a, const Seq& sq, uint32_t hk, uint32_t r0, uint32_t R, float gk) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint32_t r = r0 + 8u * nt + g;
@@ -492,16 +490,20 @@ struct Work {
   int32_t lo, hi, base;  // tokens that any query sees; base: of unit 0
   uint32_t R, tiles, span;
 };
+// From w.s, which has queries.
 template <int ROWS, int UNIT>
-__device__ __forceinline__ bool work_of(const AttnArgs& a, uint32_t b, Work& w) {
-  w.tiles = w.span = 0;
-  if (!seq_of(a, b, w.s) || w.s.n == 0) return false;
+__device__ __forceinline__ void lay_out(const AttnArgs& a, Work& w) {
   w.R = w.s.n * a.G;
   w.tiles = (w.R + ROWS - 1u) / ROWS;
   w.lo = tile_range(a, w.s, 0, 0).lo;
   w.hi = tile_range(a, w.s, w.s.n - 1, w.s.n - 1).hi;
   w.base = w.lo & ~(UNIT - 1);
   w.span = w.hi > w.lo ? ((uint32_t)(w.hi - w.base) + UNIT - 1u) / UNIT : 1u;  // an empty range is one unit of nothing
+}
+template <int ROWS, int UNIT>
+__device__ __forceinline__ bool work_of(const AttnArgs& a, uint32_t b, Work& w) {
+  if (!seq_of(a, b, w.s) || w.s.n == 0) return false;
+  lay_out<ROWS, UNIT>(a, w);
   return true;
 }
 
@@ -510,13 +512,12 @@ template <int ROWS, int UNIT>
 struct Cursor {
   uint32_t b, tile, hk, off;
   Work w;
-  // Unit `at` of sequence b.
-  __device__ __forceinline__ void start(const AttnArgs& a, uint32_t b_, uint64_t at) {
-    b = b_;
-    work_of<ROWS, UNIT>(a, b, w);
-    const uint64_t q = at / w.span;
+  // Unit `at` of sequence b, w.s.
+  __device__ __forceinline__ void start(const AttnArgs& a, uint64_t at) {
+    lay_out<ROWS, UNIT>(a, w);
+    const uint64_t q = at >> 32 ? at / w.span : (uint32_t)at / w.span;
     off = (uint32_t)(at - q * w.span);
-    tile = (uint32_t)(q / a.heads);
+    tile = q >> 32 ? (uint32_t)(q / a.heads) : (uint32_t)q / a.heads;
     hk = (uint32_t)(q - (uint64_t)tile * a.heads);
   }
   // The next range's first unit; false past the last sequence.
@@ -537,6 +538,19 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
                "r"(bar)
                : "memory");
+}
+
+// total * i / n (i <= n <= 2^10).
+__device__ __forceinline__ uint64_t scaled(uint64_t total, uint32_t i, uint32_t n) {
+  if (total < (1u << 22)) return (uint32_t)total * i / n;
+  return total * i / n;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on the barrier when this thread's copy16s so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Waits with a hint of how long (in ns) the thread may be suspended; at most
@@ -568,79 +582,72 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   extern __shared__ __align__(128) uint8_t stage_mem[];  // ST units: K codes, V codes, K scales, V scales
   __shared__ __align__(8) uint64_t full[ST], empty[ST];
   __shared__ uint32_t got[ST][UNIT / 32];                 // a bit for each of the unit's tokens: it is there
-  __shared__ uint64_t wsum[kDecWarps + 1], found_at;
-  __shared__ uint32_t found_b;
   __shared__ volatile int abort_flag;
   __shared__ float sm[kDecWarps][ROWS], sl[kDecWarps][ROWS];
-  __shared__ __align__(16) float so[kDecWarps / 2][ROWS * DP];
+  __shared__ __align__(16) float so[kDecWarps][ROWS * DP];
+  __shared__ int64_t rows[UNIT];                          // pages that end inside a 16-token piece: row of each token, or -1
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t rb = a.D * Fmt<MODE>::bits / 8u, sb = a.D / Fmt<MODE>::group;
   const uint32_t v_at = UNIT * rb, ks_at = 2u * v_at, vs_at = ks_at + UNIT * sb, unit_bytes = 2u * UNIT * (rb + sb);
+  // All units, then this worker's run [u0, u1) of them and the sequence it
+  // begins in, 32 sequences at a time (every warp for itself: nothing to wait
+  // for but the lengths).
+  Work w;
+  auto units_of = [&](uint32_t b) -> uint64_t {
+    return b < a.B && work_of<ROWS, UNIT>(a, b, w) ? (uint64_t)w.tiles * a.heads * w.span : 0;
+  };
+  const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f, gv = a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f;
+  uint64_t total = 0, mine = 0;  // the first 32 sequences last: they are mostly all
+  for (uint32_t b0 = (a.B - 1u) & ~31u;; b0 -= 32u) {
+    mine = units_of(b0 + lane);
+    total += mine;
+    if (b0 == 0) break;
+  }
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < ST; ++i) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_u32(&full[i])), "r"(1));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_u32(&full[i])), "r"(a.page_size % 16u ? 33 : 1));  // without bulk copies every lane arrives
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_u32(&empty[i])), "r"((int)kDecWarps));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-
-  // All units, then this worker's run [u0, u1) of them and the sequence it
-  // begins in: kDecThreads sequences at a time.
-  auto units_of = [&](uint32_t b) -> uint64_t {
-    Work w;
-    return b < a.B && work_of<ROWS, UNIT>(a, b, w) ? (uint64_t)w.tiles * a.heads * w.span : 0;
-  };
-  const uint64_t mine = units_of(threadIdx.x);
-  uint64_t total = mine;
-  for (uint32_t b = threadIdx.x + kDecThreads; b < a.B; b += kDecThreads) total += units_of(b);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  if (lane == 0) wsum[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w <= kDecWarps; ++w) total += wsum[w];
   const uint32_t workers = (uint32_t)min((uint64_t)gridDim.x, total);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= workers) {
     if (a.split && threadIdx.x == 0) a.part_head[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  const uint64_t u0 = total * blockIdx.x / workers, u1 = total * (blockIdx.x + 1) / workers;
+  const uint64_t u0 = scaled(total, blockIdx.x, workers), u1 = scaled(total, blockIdx.x + 1, workers);
   uint64_t before = 0;  // units of the sequences before this round's
-  if (threadIdx.x == 0) found_b = a.B;
-  for (uint32_t b0 = 0; b0 < a.B; b0 += kDecThreads) {
-    const uint64_t v = b0 ? units_of(b0 + threadIdx.x) : mine;
+  Cursor<ROWS, UNIT> at;
+  at.b = a.B;
+  uint64_t found_at = 0;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += 32u) {
+    const uint64_t v = b0 ? units_of(b0 + lane) : mine;
     uint64_t incl = v;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, incl, x);
       if (lane >= (uint32_t)x) incl += y;
     }
-    __syncthreads();  // wsum is read
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    uint64_t round = 0;
-#pragma unroll
-    for (int w = 0; w <= kDecWarps; ++w) {
-      if ((uint32_t)w < warp) incl += wsum[w];
-      round += wsum[w];
-    }
-    if (u0 < before + round) {
-      incl += before;
-      if (u0 < incl && u0 >= incl - v) {
-        found_b = b0 + threadIdx.x;
-        found_at = incl - v;
-      }
+    incl += before;
+    const uint32_t past = __ballot_sync(0xffffffffu, u0 < incl);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      at.b = b0 + (uint32_t)src;
+      at.w.s.t0 = __shfl_sync(0xffffffffu, w.s.t0, src);
+      at.w.s.n = __shfl_sync(0xffffffffu, w.s.n, src);
+      at.w.s.L = __shfl_sync(0xffffffffu, w.s.L, src);
+      found_at = __shfl_sync(0xffffffffu, incl - v, src);
       break;
     }
-    before += round;
+    before = __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  if (found_b >= a.B) return;  // the lengths changed meanwhile
-
-  Cursor<ROWS, UNIT> at;
-  at.start(a, found_b, u0 - found_at);
+  __syncthreads();  // the barriers stand
+  if (at.b >= a.B) return;  // the lengths changed meanwhile
+  at.start(a, u0 - found_at);
   uint64_t u = u0;
   bool more = true;
   if (!a.split && at.off) {  // without partial results a range belongs to the worker it begins in
@@ -656,7 +663,6 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
     const uint32_t run = min((uint32_t)UNIT, a.page_size & (0u - a.page_size));
     uint32_t it = 0;
     bool ok = true;
-    int64_t row = -1;  // of this lane's run in the unit to come, looked up a unit ahead
     while (more && ok) {
       const uint32_t n = take();
       const int32_t* table = a.page_table + (uint64_t)at.b * a.max_pages;
@@ -668,10 +674,21 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
         atomicOr(&g_device_error, (unsigned)kDevErrIndex);
         return -1;
       };
+      // runs of at least 16 tokens: lane = run * 4 + part; else token lane + 32 i
       const uint32_t part = lane & 3u, r = lane >> 2;
-      auto look = [&](uint32_t k) {  // 16-token pieces at least: lane = run * 4 + part
-        const int32_t j = at.w.base + (int32_t)((at.off + k) * UNIT + r * run);
-        row = run >= 16u && r * run < (uint32_t)UNIT && j < at.w.hi && j + (int32_t)run > at.w.lo ? row_of(j) : -1;
+      int64_t y[UNIT / 32];  // rows of the unit to come, looked up a unit ahead
+      auto look = [&](uint32_t k) {
+        const int32_t t0 = at.w.base + (int32_t)((at.off + k) * UNIT);
+        if (run >= 16u) {
+          const int32_t j = t0 + (int32_t)(r * run);
+          y[0] = r * run < (uint32_t)UNIT && j < at.w.hi && j + (int32_t)run > at.w.lo ? row_of(j) : -1;
+        } else {
+#pragma unroll
+          for (int i = 0; i < UNIT / 32; ++i) {
+            const int32_t j = t0 + (int32_t)(32u * i + lane);
+            y[i] = j >= at.w.lo && j < at.w.hi ? row_of(j) : -1;
+          }
+        }
       };
       if (n > 0) look(0);
       for (uint32_t k = 0; k < n; ++k, ++it) {
@@ -684,7 +701,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
         const uint32_t bar = shared_u32(&full[st]), dst = shared_u32(stage_mem) + st * unit_bytes;
         if (run >= 16u) {
           const int32_t j = t0 + (int32_t)(r * run);
-          const uint32_t cnt = row >= 0 ? min(run, ((uint32_t)(at.w.hi - j) + 15u) & ~15u) : 0u;
+          const uint32_t cnt = y[0] >= 0 ? min(run, ((uint32_t)(at.w.hi - j) + 15u) & ~15u) : 0u;
           uint32_t tokens = 0;
 #pragma unroll
           for (int i = 0; i < UNIT / 32; ++i) {
@@ -699,42 +716,44 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
           if (cnt) {
             const uint32_t bytes = part < 2u ? rb : sb;
             const uint8_t* src = part == 0 ? a.codes[0] : part == 1 ? a.codes[1] : part == 2 ? a.scales[0] : a.scales[1];
-            bulk_copy(dst + (part == 0 ? 0u : part == 1 ? v_at : part == 2 ? ks_at : vs_at) + r * run * bytes, src + (uint64_t)row * bytes,
+            bulk_copy(dst + (part == 0 ? 0u : part == 1 ? v_at : part == 2 ? ks_at : vs_at) + r * run * bytes, src + (uint64_t)y[0] * bytes,
                       cnt * bytes, bar);
           }
-          if (k + 1 < n) look(k + 1);
         } else {
-          // pages that end inside a 16-token piece: token by token, scales by
-          // plain loads (their rows need not be 16 bytes long)
-          int64_t y[UNIT / 32];
-          uint32_t tokens = 0;
+          // pages that end inside a 16-token piece: codes by 16-byte pieces of
+          // each token's row, scales (rows of any few bytes) by plain loads
 #pragma unroll
           for (int i = 0; i < UNIT / 32; ++i) {
-            const uint32_t x = 32u * i + lane;
-            const int32_t j = t0 + (int32_t)x;
-            y[i] = j >= at.w.lo && j < at.w.hi ? row_of(j) : -1;
+            rows[32u * i + lane] = y[i];
             const uint32_t mask = __ballot_sync(0xffffffffu, y[i] >= 0);
             if (lane == 0) got[st][i] = mask;
-            tokens += __popc(mask);
-            uint8_t* sc = stage_mem + st * unit_bytes + ks_at + x * sb;
-            for (uint32_t e = 0; y[i] >= 0 && e < sb; ++e) {
-              sc[e] = __ldg(a.scales[0] + (uint64_t)y[i] * sb + e);
-              sc[UNIT * sb + e] = __ldg(a.scales[1] + (uint64_t)y[i] * sb + e);
+          }
+          __syncwarp();
+          const uint32_t per = rb / 16u;
+#pragma unroll 4
+          for (uint32_t x = lane; x < UNIT * per; x += 32u) {
+            const int64_t row = rows[x / per];
+            if (row >= 0) {
+              const uint64_t from = (uint64_t)row * rb + (x % per) * 16u;
+              copy16(dst + x * 16u, a.codes[0] + from);
+              copy16(dst + v_at + x * 16u, a.codes[1] + from);
+            }
+          }
+          copies_arrive(bar);
+#pragma unroll 4
+          for (uint32_t x = lane; x < UNIT * sb; x += 32u) {
+            const int64_t row = rows[x / sb];
+            if (row >= 0) {
+              const uint64_t from = (uint64_t)row * sb + x % sb;
+              uint8_t* to = stage_mem + st * unit_bytes + ks_at + x;
+              to[0] = __ldg(a.scales[0] + from);
+              to[UNIT * sb] = __ldg(a.scales[1] + from);
             }
           }
           __syncwarp();
-          if (lane == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(tokens * 2u * rb) : "memory");
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < UNIT / 32; ++i) {
-            const uint32_t x = 32u * i + lane;
-            if (y[i] >= 0) {
-              bulk_copy(dst + x * rb, a.codes[0] + (uint64_t)y[i] * rb, rb, bar);
-              bulk_copy(dst + v_at + x * rb, a.codes[1] + (uint64_t)y[i] * rb, rb, bar);
-            }
-          }
+          if (lane == 0) arrive(bar);
         }
+        if (k + 1 < n) look(k + 1);
       }
       u += n;
       more = ok && u < u1 && at.next(a);
@@ -759,7 +778,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
     const uint32_t n = take(), r0 = at.tile * ROWS, R = at.w.R;
     const Seq s = at.w.s;
     const bool whole = at.off == 0 && n == at.w.span;
-    d.load_q(a, s, at.hk, r0, R);
+    d.load_q(a, s, at.hk, r0, R, gk);
     // what this lane's columns (rows r0 + 8 nt + 2c, + 1) see
     int32_t see_lo[NT][2], see_hi[NT][2];
 #pragma unroll
@@ -881,7 +900,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
       if (lane == 0) arrive(shared_u32(&empty[st]));
     }
 
-    // Join the warps: a common maximum first, then the sums, two warps at a time.
+    // Join the warps: a common maximum first, then the sums.
     auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -912,71 +931,59 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
         }
       }
 #pragma unroll
-    for (int half = kDecWarps / 2; half > 0; half >>= 1) {
-      if (warp >= (uint32_t)half && warp < 2u * half) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
+        reinterpret_cast<float4*>(so[warp])[(nt * MT + mt) * 32 + lane] =
+            make_float4(d.o[nt][mt][0], d.o[nt][mt][1], d.o[nt][mt][2], d.o[nt][mt][3]);
+    sync();
+    // eight elements (m-tiles 4k .. 4k + 3) of the lane's columns 2c + e of n-tile nt
+    const uint32_t slot = 2u * blockIdx.x + (seg ? 1u : 0u);
+    const float fv = D::kMx ? 0x1p64f : gv;
+#pragma unroll 1
+    for (uint32_t item = warp; item < NT * (DP / 64) * 2u; item += kDecWarps) {
+      const uint32_t e = item & 1u, k = (item >> 1) % (DP / 64), nt = (item >> 1) / (DP / 64);
+      const uint32_t lr = 8u * nt + 2u * d.c + e, r = r0 + lr, el = d.g * (DP / 8) + 8u * k;
+      if (r >= R || el >= a.D) continue;
+      float M = -INFINITY, l = 0.0f;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            reinterpret_cast<float4*>(so[warp - half])[(nt * MT + mt) * 32 + lane] =
-                make_float4(d.o[nt][mt][0], d.o[nt][mt][1], d.o[nt][mt][2], d.o[nt][mt][3]);
+      for (int w = 0; w < kDecWarps; ++w) {
+        M = fmaxf(M, sm[w][lr]);
+        l += sl[w][lr];
       }
-      sync();
-      if (warp < (uint32_t)half) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const float4 v = reinterpret_cast<const float4*>(so[warp])[(nt * MT + mt) * 32 + lane];
-            d.o[nt][mt][0] += v.x;
-            d.o[nt][mt][1] += v.y;
-            d.o[nt][mt][2] += v.z;
-            d.o[nt][mt][3] += v.w;
-          }
+      const uint32_t i = r / a.G, h = at.hk * a.G + (r - i * a.G);
+      const uint64_t to = (uint64_t)(s.t0 + i) * a.Hq + h;
+      const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
+      if (d.g == 0 && k == 0) {
+        if (!whole) a.part_ml[slot * ROWS + lr] = make_float2(M, l);
+        else if (a.lse) a.lse[to] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
       }
-      sync();
-    }
-    if (warp == 0) {
-      const uint32_t slot = 2u * blockIdx.x + (seg ? 1u : 0u);
-      const float fv = D::kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
+      float v[8];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < 4; ++x) {
+        v[2 * x] = v[2 * x + 1] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t lr = 8u * nt + 2u * d.c + e, r = r0 + lr;
-          if (r >= R) continue;
-          float l = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) l += sl[w][lr];
-          const uint32_t i = r / a.G, h = at.hk * a.G + (r - i * a.G);
-          const uint64_t to = (uint64_t)(s.t0 + i) * a.Hq + h;
-          const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
-          if (whole) {
-            if (a.lse && d.g == 0) a.lse[to] = l > 0.0f ? (d.m[nt][e] + log2f(l)) * kLn2 : -INFINITY;
-          } else if (d.g == 0) {
-            a.part_ml[slot * ROWS + lr] = make_float2(d.m[nt][e], l);
-          }
-#pragma unroll
-          for (int k = 0; k < DP / 64; ++k) {  // eight elements: m-tiles 4k .. 4k + 3
-            const uint32_t el = d.g * (DP / 8) + 8u * k;
-            if (el >= a.D) continue;
-            float v[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              v[2 * x] = d.o[nt][4 * k + x][e] * f;
-              v[2 * x + 1] = d.o[nt][4 * k + x][2 + e] * f;
-            }
-            if (whole)
-              store8<QT>(static_cast<QT*>(a.out) + to * a.D + el, v);
-            else
-              store8<float>(a.part_o + ((uint64_t)slot * ROWS + lr) * a.D + el, v);
-          }
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float4 p = reinterpret_cast<const float4*>(so[w])[(nt * MT + 4u * k + x) * 32u + lane];
+          v[2 * x] += e ? p.y : p.x;
+          v[2 * x + 1] += e ? p.w : p.z;
         }
+        v[2 * x] *= f;
+        v[2 * x + 1] *= f;
+      }
+      if (whole)
+        store8<QT>(static_cast<QT*>(a.out) + to * a.D + el, v);
+      else
+        store8<float>(a.part_o + ((uint64_t)slot * ROWS + lr) * a.D + el, v);
+    }
+    sync();  // so, sm and sl are read
+    if (warp == 0) {
       // The worker that begins a range it does not end says which workers have
       // the rest: the next ones, each in its first slot.
       if (!whole && at.off == 0 && lane == 0) {
         const uint64_t last = u + at.w.span - 1u;  // the range's last unit
-        const uint32_t worker = (uint32_t)(((last + 1u) * workers - 1u) / total);
+        const uint64_t top = (last + 1u) * workers - 1u;
+        const uint32_t worker = top >> 32 || total >> 32 ? (uint32_t)(top / total) : (uint32_t)top / (uint32_t)total;
         a.part_head[2 * blockIdx.x] = make_int4((int)worker + 1, (int)slot, (int)(s.t0 + r0 / a.G), (int)min((uint32_t)ROWS, R - r0));
         a.part_head[2 * blockIdx.x + 1] = make_int4((int)(r0 % a.G), (int)at.hk, 0, 0);
       }
@@ -986,19 +993,19 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   }
 }
 
-// Join of one row (blockIdx.y) of the range that worker blockIdx.x began and
-// others went on with: a warp for every fourth part, the row's elements over
-// the lanes.
+// Join of two rows (2 blockIdx.y, + 1) of the range that worker blockIdx.x
+// began and others went on with: four warps a row, one for every fourth part,
+// the row's elements over the lanes.
 template <typename QT, int ROWS>
-__global__ void __launch_bounds__(128) k_kv_decode_join(const __grid_constant__ AttnArgs a) {
-  __shared__ float sl[4];
-  __shared__ __align__(16) float so[4][256];
+__global__ void __launch_bounds__(256) k_kv_decode_join(const __grid_constant__ AttnArgs a) {
+  __shared__ float sl[8];
+  __shared__ __align__(16) float so[8][256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 head = a.part_head[2 * blockIdx.x], more = a.part_head[2 * blockIdx.x + 1];
-  const uint32_t lr = blockIdx.y;
-  if (head.x == 0 || lr >= (uint32_t)head.w) return;
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const uint32_t parts = (uint32_t)head.x - blockIdx.x, d0 = lane * 8u;
+  const int4 head = a.part_head[2 * blockIdx.x];
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, lr = 2u * blockIdx.y + (warp >> 2), w0 = warp & ~3u;
+  if (head.x == 0 || 2u * blockIdx.y >= (uint32_t)head.w) return;
+  const int4 more = a.part_head[2 * blockIdx.x + 1];
+  const uint32_t parts = lr < (uint32_t)head.w ? (uint32_t)head.x - blockIdx.x : 0u, d0 = lane * 8u;
   auto slot = [&](uint32_t k) { return k == 0 ? (uint32_t)head.y : 2u * (blockIdx.x + k); };
   float m = -INFINITY;
   for (uint32_t k = lane; k < parts; k += 32) m = fmaxf(m, a.part_ml[slot(k) * ROWS + lr].x);
@@ -1008,33 +1015,30 @@ __global__ void __launch_bounds__(128) k_kv_decode_join(const __grid_constant__ 
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = 0.0f;
 #pragma unroll 4
-  for (uint32_t k = warp; k < parts; k += 4) {
+  for (uint32_t k = warp & 3u; k < parts; k += 4u) {
     const float2 ml = a.part_ml[slot(k) * ROWS + lr];
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (d0 < a.D) load8_shared<float>(a.part_o + ((uint64_t)slot(k) * ROWS + lr) * a.D + d0, v);
     const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
     l += ml.y * f;
-    if (d0 < a.D) {
-      float v[8];
-      load8_shared<float>(a.part_o + ((uint64_t)slot(k) * ROWS + lr) * a.D + d0, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e], f, o[e]);
-    }
+    for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e], f, o[e]);
   }
   if (lane == 0) sl[warp] = l;
-  if (d0 < a.D) store8<float>(&so[warp][d0], o);
+  store8<float>(&so[warp][d0], o);
   __syncthreads();
-  if (warp != 0) return;
-  l = sl[0] + sl[1] + sl[2] + sl[3];
+  if (warp != w0 || parts == 0) return;
+  l = sl[w0] + sl[w0 + 1] + sl[w0 + 2] + sl[w0 + 3];
   const uint32_t x = (uint32_t)more.x + lr, i = x / a.G;  // query after the tile's first, head of the group
   const uint64_t at = (uint64_t)((uint32_t)head.z + i) * a.Hq + (uint32_t)more.y * a.G + (x - i * a.G);
   if (a.lse && lane == 0) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
   if (d0 >= a.D) return;
-  float v[8];
+  const float f = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = so[0][d0 + e] + so[1][d0 + e] + so[2][d0 + e] + so[3][d0 + e];
-    v[e] = l > 0.0f ? v[e] / l : 0.0f;
-  }
-  store8<QT>(static_cast<QT*>(a.out) + at * a.D + d0, v);
+  for (int e = 0; e < 8; ++e) o[e] = (so[w0][d0 + e] + so[w0 + 1][d0 + e] + so[w0 + 2][d0 + e] + so[w0 + 3][d0 + e]) * f;
+  store8<QT>(static_cast<QT*>(a.out) + at * a.D + d0, o);
 }
 
 // k_kv_prefill's join.  One (query, head): one CTA, a warp for every

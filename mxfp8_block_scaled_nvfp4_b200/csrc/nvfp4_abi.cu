@@ -1087,8 +1087,8 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
         // the join's launch overlaps the kernel before it
         cudaLaunchConfig_t cfg;
         memset(&cfg, 0, sizeof(cfg));
-        cfg.gridDim = dim3((unsigned)grid, ROWS);
-        cfg.blockDim = dim3(128);
+        cfg.gridDim = dim3((unsigned)grid, ROWS / 2);
+        cfg.blockDim = dim3(256);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
