@@ -108,12 +108,13 @@ __device__ __forceinline__ float ex2(float x) {
 //
 // In a CTA a fifth warp copies the units ahead into shared memory, so loads
 // cost the other four neither instructions nor registers: one bulk copy a page
-// (or piece of one) and part (K and V codes, K and V scales); each of those takes 16 * TS tokens of every unit, with its own
-// running maximum, and they join at the end of a range.  Codes go from shared
-// memory straight into matrix fragments: a quad of lanes holds one token's
-// key row (the order of the elements along D is free as long as q's fragments
-// use the same), and a lane's share of a value row is the D / 8 consecutive
-// elements of its fragment rows.
+// (or piece of one) and part (K and V codes, K and V scales).  Each of the four
+// takes 16 * TS tokens of every unit, with its own running maximum, and they
+// join at the end of a range.  Codes go from shared memory straight into
+// matrix fragments: a quad of lanes holds one token's key row (the order of
+// the elements along D is free as long as q's fragments use the same), and a
+// lane's share of a value row is the D / 8 consecutive elements of its
+// fragment rows.
 //   S^T [16 tokens x 8 rows] = K_hat . q^T      (m16n8k16, fp32)
 //   O^T [16 elements x 8 rows] += V_hat^T . P^T
 // P^T is S^T's fragment transposed by movmatrix.
@@ -513,12 +514,12 @@ struct Cursor {
   uint32_t b, tile, hk, off;
   Work w;
   // Unit `at` of sequence b, w.s.
-  __device__ __forceinline__ void start(const AttnArgs& a, uint64_t at) {
+  __device__ __forceinline__ void start(const AttnArgs& a, uint32_t at) {
     lay_out<ROWS, UNIT>(a, w);
-    const uint64_t q = at >> 32 ? at / w.span : (uint32_t)at / w.span;
-    off = (uint32_t)(at - q * w.span);
-    tile = q >> 32 ? (uint32_t)(q / a.heads) : (uint32_t)q / a.heads;
-    hk = (uint32_t)(q - (uint64_t)tile * a.heads);
+    const uint32_t q = at / w.span;
+    off = at - q * w.span;
+    tile = q / a.heads;
+    hk = q - tile * a.heads;
   }
   // The next range's first unit; false past the last sequence.
   __device__ __forceinline__ bool next(const AttnArgs& a) {
@@ -540,11 +541,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// total * i / n (i <= n <= 2^10).
-__device__ __forceinline__ uint64_t scaled(uint64_t total, uint32_t i, uint32_t n) {
-  if (total < (1u << 22)) return (uint32_t)total * i / n;
-  return total * i / n;
-}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -593,11 +589,12 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   // begins in, 32 sequences at a time (every warp for itself: nothing to wait
   // for but the lengths).
   Work w;
-  auto units_of = [&](uint32_t b) -> uint64_t {
-    return b < a.B && work_of<ROWS, UNIT>(a, b, w) ? (uint64_t)w.tiles * a.heads * w.span : 0;
+  // (The caller's bounds keep the number of units below 2^32.)
+  auto units_of = [&](uint32_t b) -> uint32_t {
+    return b < a.B && work_of<ROWS, UNIT>(a, b, w) ? w.tiles * a.heads * w.span : 0u;
   };
   const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f, gv = a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f;
-  uint64_t total = 0, mine = 0;  // the first 32 sequences last: they are mostly all
+  uint32_t total = 0, mine = 0;  // the first 32 sequences last: they are mostly all
   for (uint32_t b0 = (a.B - 1u) & ~31u;; b0 -= 32u) {
     mine = units_of(b0 + lane);
     total += mine;
@@ -613,23 +610,25 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  const uint32_t workers = (uint32_t)min((uint64_t)gridDim.x, total);
+  const uint32_t workers = min(gridDim.x, total);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= workers) {
     if (a.split && threadIdx.x == 0) a.part_head[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  const uint64_t u0 = scaled(total, blockIdx.x, workers), u1 = scaled(total, blockIdx.x + 1, workers);
-  uint64_t before = 0;  // units of the sequences before this round's
+  // the first `longer` workers take one unit more than the others
+  const uint32_t each = total / workers, longer = total - each * workers;
+  const uint32_t u0 = each * blockIdx.x + min(blockIdx.x, longer), u1 = u0 + each + (blockIdx.x < longer ? 1u : 0u);
+  uint32_t before = 0;  // units of the sequences before this round's
   Cursor<ROWS, UNIT> at;
   at.b = a.B;
-  uint64_t found_at = 0;
+  uint32_t found_at = 0;
   for (uint32_t b0 = 0; b0 < a.B; b0 += 32u) {
-    const uint64_t v = b0 ? units_of(b0 + lane) : mine;
-    uint64_t incl = v;
+    const uint32_t v = b0 ? units_of(b0 + lane) : mine;
+    uint32_t incl = v;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, incl, x);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, x);
       if (lane >= (uint32_t)x) incl += y;
     }
     incl += before;
@@ -648,14 +647,14 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   __syncthreads();  // the barriers stand
   if (at.b >= a.B) return;  // the lengths changed meanwhile
   at.start(a, u0 - found_at);
-  uint64_t u = u0;
+  uint32_t u = u0;
   bool more = true;
   if (!a.split && at.off) {  // without partial results a range belongs to the worker it begins in
     u += at.w.span - at.off;
     more = u < u1 && at.next(a);
   }
   // units of the current range that this worker takes
-  auto take = [&]() { return a.split ? (uint32_t)min((uint64_t)(at.w.span - at.off), u1 - u) : at.w.span; };
+  auto take = [&]() { return a.split ? min(at.w.span - at.off, u1 - u) : at.w.span; };
 
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ copies
@@ -981,9 +980,8 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
       // The worker that begins a range it does not end says which workers have
       // the rest: the next ones, each in its first slot.
       if (!whole && at.off == 0 && lane == 0) {
-        const uint64_t last = u + at.w.span - 1u;  // the range's last unit
-        const uint64_t top = (last + 1u) * workers - 1u;
-        const uint32_t worker = top >> 32 || total >> 32 ? (uint32_t)(top / total) : (uint32_t)top / (uint32_t)total;
+        const uint32_t last = u + at.w.span - 1u, many = longer * (each + 1u);
+        const uint32_t worker = last < many ? last / (each + 1u) : longer + (last - many) / each;
         a.part_head[2 * blockIdx.x] = make_int4((int)worker + 1, (int)slot, (int)(s.t0 + r0 / a.G), (int)min((uint32_t)ROWS, R - r0));
         a.part_head[2 * blockIdx.x + 1] = make_int4((int)(r0 % a.G), (int)at.hk, 0, 0);
       }

@@ -1062,6 +1062,8 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
     if (product_exceeds(tiles, p.chunks, INT32_MAX) || product_exceeds(tiles * p.chunks, B * cache->heads, INT32_MAX))
       return fail(NVFP4_ERR_INVALID_ARG, "[%s] max_q, max_kv and B too large together", tag);
   } else {
+    if ((double)B * (double)cache->heads * (double)tiles * ((double)max_kv / 64 + 2) >= 4294967296.0)
+      return fail(NVFP4_ERR_UNSUPPORTED, "[%s] B, heads, max_q and max_kv too large together: lower the bounds", tag);
     workers = (int64_t)(workspace_bytes / p.bytes_per_chunk);
     if (workers > kKvMaxWorkers) workers = kKvMaxWorkers;
     a.split = workers >= kKvWorkers && max_kv > 64;
