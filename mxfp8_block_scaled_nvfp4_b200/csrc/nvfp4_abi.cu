@@ -843,6 +843,11 @@ static bool bad_stride(int64_t T, int64_t stride, int64_t width, nvfp4_dtype dt)
   return T > 1 && (stride < width || stride > INT32_MAX || stride * dt_size(dt) % 16 != 0);
 }
 
+// Every row (of a multiple of 32 elements) begins at a multiple of 32 bytes.
+static bool rows_aligned32(const void* p, int64_t T, int64_t stride, nvfp4_dtype dt) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (T <= 1 || stride * dt_size(dt) % 32 == 0);
+}
+
 static kv::RowArgs kv_row_args(const nvfp4_kv_cache* c, int64_t T, const int32_t* slots) {
   kv::RowArgs a;
   memset(&a, 0, sizeof(a));
@@ -887,10 +892,15 @@ nvfp4_status kv_cache_write(const nvfp4_kv_cache* cache, const void* k, const vo
   a.x[1] = v;
   a.stride[0] = k_stride;
   a.stride[1] = v_stride;
+  const bool v8 = rows_aligned32(k, T, k_stride, dt) && rows_aligned32(v, T, v_stride, dt);
   const dim3 grid((a.units + kv::kRowThreads - 1) / kv::kRowThreads, 2);
   dispatch_dt(dt, [&](auto tag_t) {
     using E = decltype(tag_t);
-    dispatch_mode(cache->mode, [&](auto m) { kv::k_kv_write<E, decltype(m)::value><<<grid, kv::kRowThreads, 0, stream>>>(a); });
+    dispatch_mode(cache->mode, [&](auto m) {
+      constexpr int MODE = decltype(m)::value;
+      if (v8) kv::k_kv_write<E, MODE, true><<<grid, kv::kRowThreads, 0, stream>>>(a);
+      else kv::k_kv_write<E, MODE, false><<<grid, kv::kRowThreads, 0, stream>>>(a);
+    });
   });
   return check_launch(tag);
 }
@@ -914,10 +924,15 @@ nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
   a.x[0] = k_out;
   a.x[1] = v_out;
   a.stride[0] = a.stride[1] = width;
+  const bool v8 = rows_aligned32(k_out, T, width, out_dt) && rows_aligned32(v_out, T, width, out_dt);
   const dim3 grid((a.units + kv::kRowThreads - 1) / kv::kRowThreads, 2);
   dispatch_dt(out_dt, [&](auto tag_t) {
     using E = decltype(tag_t);
-    dispatch_mode(cache->mode, [&](auto m) { kv::k_kv_read<E, decltype(m)::value><<<grid, kv::kRowThreads, 0, stream>>>(a); });
+    dispatch_mode(cache->mode, [&](auto m) {
+      constexpr int MODE = decltype(m)::value;
+      if (v8) kv::k_kv_read<E, MODE, true><<<grid, kv::kRowThreads, 0, stream>>>(a);
+      else kv::k_kv_read<E, MODE, false><<<grid, kv::kRowThreads, 0, stream>>>(a);
+    });
   });
   return check_launch(tag);
 }

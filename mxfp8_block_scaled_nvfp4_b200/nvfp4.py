@@ -12,6 +12,7 @@ torch and pass device pointers plus ``torch.cuda.current_stream()``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -116,7 +117,9 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device as a pointer (the raw handle:
+    building a torch.cuda.Stream object takes longer than a small launch)."""
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _need_cuda(*ts):
@@ -582,24 +585,29 @@ class KvCache:
         return cls(mode, *t, g_k, g_v)
 
 
-def _need_rows(t, shape, what: str):
-    """[T, heads, D] on the current device, heads and D contiguous, any token
-    stride (a part of a longer row is taken as it is)."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {tuple(shape)}, got {tuple(t.shape)}")
+def _need_rows(t, shape, what: str, dev: int):
+    """[T, heads, D] on the current device `dev`, heads and D contiguous, any
+    token stride (a part of a longer row is taken as it is)."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} on {t.device}, but the current device is cuda:{torch.cuda.current_device()}; "
+    if t.device.index != dev:
+        raise ValueError(f"{what} on {t.device}, but the current device is cuda:{dev}; "
                          "call under torch.cuda.device(tensor.device)")
-    if t.numel() and ((t.stride(2) != 1 and shape[2] > 1) or (t.stride(1) != shape[2] and shape[1] > 1)):
+    st = t.stride()
+    if t.numel() and ((st[2] != 1 and shape[2] > 1) or (st[1] != shape[2] and shape[1] > 1)):
         raise ValueError(f"{what}: heads and D must be contiguous")
+    return st[0]
 
 
-def _need_cache(cache):
-    if cache.device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {cache.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device(cache.device)")
+def _need_cache(cache) -> int:
+    """The current device, which has to be the cache's."""
+    dev = torch.cuda.current_device()
+    if cache.device.index != dev:
+        raise ValueError(f"the cache is on {cache.device}, but the current device is cuda:{dev}; "
+                         "call under torch.cuda.device(cache.device)")
+    return dev
 
 
 def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
@@ -610,11 +618,10 @@ def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torc
         raise ValueError("k and v must share a dtype: float32, float16 or bfloat16")
     _need_dtype(slots, torch.int32, "slots")
     _need_cuda(slots)
-    _need_cache(cache)
-    _need_rows(k, shape, "k")
-    _need_rows(v, shape, "v")
-    _check(lib().kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), DT[k.dtype], shape[0], k.stride(0),
-                                v.stride(0), slots.data_ptr(), _stream()))
+    dev = _need_cache(cache)
+    k_stride, v_stride = _need_rows(k, shape, "k", dev), _need_rows(v, shape, "v", dev)
+    _check(lib().kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), DT[k.dtype], shape[0], k_stride, v_stride,
+                                slots.data_ptr(), _stream()))
 
 
 def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None):
@@ -638,6 +645,7 @@ def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_o
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=4096)
 def kv_attention_workspace_size(B: int, T: int, Hq: int, heads: int, D: int, max_q: int = 1, max_kv: int = 0,
                                 window: int = 0) -> int:
     return int(lib().kv_attention_workspace_size(B, T, Hq, heads, D, max_q, max_kv, window))
@@ -657,20 +665,29 @@ def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_l
     the page table; tight bounds are faster).  scale defaults to D ** -0.5.
     workspace: uint8 scratch of kv_attention_workspace_size bytes (allocated
     here when None)."""
-    T, Hq = q.shape[0], q.shape[1]
+    T, Hq, D = q.shape
     B, max_pages = page_table.shape
-    _need_dtype(page_table, torch.int32, "page_table")
-    _need_dtype(kv_len, torch.int32, "kv_len")
-    _need_bytes(kv_len, 4 * B, "kv_len")
-    _need_dtype(q_start, torch.int32, "q_start")
-    _need_bytes(q_start, 4 * (B + 1), "q_start")
-    _need_dtype(out, q.dtype, "out")
-    _need_bytes(out, T * Hq * cache.D * q.element_size(), "out")
-    _need_dtype(lse, torch.float32, "lse")
-    _need_bytes(lse, 4 * T * Hq, "lse")
-    _need_cuda(page_table, kv_len, q_start, out, lse, workspace)
-    _need_cache(cache)
-    _need_rows(q, (T, Hq, cache.D), "q")
+    # (what is None is not looked at: a decoding call is short)
+    if page_table.dtype != torch.int32 or kv_len.dtype != torch.int32 or kv_len.numel() < B:
+        _need_dtype(page_table, torch.int32, "page_table")
+        _need_dtype(kv_len, torch.int32, "kv_len")
+        _need_bytes(kv_len, 4 * B, "kv_len")
+    _need_cuda(page_table, kv_len)
+    if q_start is not None:
+        _need_dtype(q_start, torch.int32, "q_start")
+        _need_bytes(q_start, 4 * (B + 1), "q_start")
+        _need_cuda(q_start)
+    if out is not None:
+        _need_dtype(out, q.dtype, "out")
+        _need_bytes(out, T * Hq * D * q.element_size(), "out")
+        _need_cuda(out)
+    if lse is not None:
+        _need_dtype(lse, torch.float32, "lse")
+        _need_bytes(lse, 4 * T * Hq, "lse")
+        _need_cuda(lse)
+    if workspace is not None:
+        _need_cuda(workspace)
+    q_stride = _need_rows(q, (T, Hq, cache.D), "q", _need_cache(cache))
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
     if max_q is None:
@@ -678,15 +695,17 @@ def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_l
     if max_kv is None:
         max_kv = max_pages * cache.page_size
     if out is None:
-        out = torch.empty(T, Hq, cache.D, dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
     if lse is None and return_lse:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-    L = lib()
     if workspace is None:
-        size = L.kv_attention_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
-    _check(L.kv_attention(cache._ref, q.data_ptr(), DT[q.dtype], q.stride(0), _ptr(q_start), kv_len.data_ptr(),
-                          page_table.data_ptr(), B, T, Hq, max_q, max_kv, max_pages,
-                          cache.D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(), _ptr(lse),
-                          _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream()))
+        size = kv_attention_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
+        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device) if size else None
+    else:
+        size = _nbytes(workspace)
+    _check(lib().kv_attention(
+        cache._ref, q.data_ptr(), DT[q.dtype], q_stride, None if q_start is None else q_start.data_ptr(),
+        kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, max_q, max_kv, max_pages,
+        cache.D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size, _stream()))
     return out if lse is None else (out, lse)

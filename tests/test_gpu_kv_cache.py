@@ -101,6 +101,18 @@ def test_parts_of_a_projection_are_taken_as_they_lie(nv):
     nv.kv_cache_write(b, k.contiguous(), v.contiguous(), slots)
     assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
     assert torch.equal(a.k_scales, b.k_scales) and torch.equal(a.v_scales, b.v_scales)
+    # rows that begin at odd multiples of 16 bytes
+    odd = torch.empty(T, heads * D + 8, dtype=bf16, device="cuda")
+    ko, vo = odd[:, 8:].unflatten(1, (heads, D)), odd.clone()[:, 8:].unflatten(1, (heads, D))
+    ko.copy_(k)
+    vo.copy_(v)
+    nv.kv_cache_write(a, ko, vo, slots)
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
+    flat = torch.empty(2 * T * heads * D + 8, dtype=bf16, device="cuda")[8:]
+    outs = flat[:T * heads * D].view(T, heads, D), flat[T * heads * D:].view(T, heads, D)
+    nv.kv_cache_read(a, slots, k_out=outs[0], v_out=outs[1])
+    want = nv.kv_cache_read(b, slots, bf16)
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
     # every second token of a longer tensor, and one token broadcast over T
     nv.kv_cache_write(a, k[::2], v[::2], slots[::2].contiguous())
     assert torch.equal(a.k_codes, b.k_codes)

@@ -132,12 +132,12 @@ def test_binding_refuses_what_a_pointer_would_hide():
     with pytest.raises(ValueError, match="CUDA tensors"):
         nv.KvCache("mxfp8", e(4, 2, 16, 16, dtype=i32), e(4, 2, 16, 2), e(4, 2, 16, 16, dtype=i32), e(4, 2, 16, 2))
     with pytest.raises(ValueError, match="heads and D"):
-        nv._need_rows(_OnDevice((3, 2, 64), (256, 128, 1)), (3, 2, 64), "k")
-    nv._need_rows(_OnDevice((3, 2, 64), (999, 64, 1)), (3, 2, 64), "k")
+        nv._need_rows(_OnDevice((3, 2, 64), (256, 128, 1)), (3, 2, 64), "k", 0)
+    nv._need_rows(_OnDevice((3, 2, 64), (999, 64, 1)), (3, 2, 64), "k", 0)
     with pytest.raises(ValueError, match=r"must be \(3, 2, 64\)"):
-        nv._need_rows(_OnDevice((3, 2, 32), (64, 32, 1)), (3, 2, 64), "k")
+        nv._need_rows(_OnDevice((3, 2, 32), (64, 32, 1)), (3, 2, 64), "k", 0)
     with pytest.raises(ValueError, match="current device is cuda:0"):
-        nv._need_rows(_OnDevice((3, 2, 64), (128, 64, 1), 1), (3, 2, 64), "k")
+        nv._need_rows(_OnDevice((3, 2, 64), (128, 64, 1), 1), (3, 2, 64), "k", 0)
 
 
 class _OnDevice:
@@ -150,8 +150,8 @@ class _OnDevice:
     def numel(self):
         return self.shape[0] * self.shape[1] * self.shape[2]
 
-    def stride(self, i):
-        return self._strides[i]
+    def stride(self):
+        return self._strides
 
 
 @pytest.fixture(autouse=True)
