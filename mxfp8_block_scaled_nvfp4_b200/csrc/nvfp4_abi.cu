@@ -950,10 +950,14 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
                       int64_t window, bool prefill_has_it, size_t workspace_bytes) {
   KvPlan p;
   const int64_t rows = max_q * (Hq / heads);
+  // k_kv_decode decodes every code again for each 16 rows, k_kv_prefill once for
+  // 256: NVFP4, 8 heads of 128, 8 sequences of 4096 tokens, 32 rows 39 us
+  // against 49, 48 rows 49 against 51, 64 rows 60 against 53 (one sequence of
+  // 32768: 43 / 50, 58 / 51, 73 / 51)
   p.prefill = prefill_has_it && rows > 32;
   p.chunk = p.chunks = 1;
   if (!p.prefill) {
-    p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;
+    p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;  // D 256: two n-tiles would take more registers than there are
     p.bytes_per_chunk = (size_t)(2 * p.tile_rows * (D * 4 + 8) + 32);
     return p;
   }

@@ -74,6 +74,35 @@ def test_one_token_a_sequence(nv, mode, dtype, heads, G, D, page_size):
     compare(nv, c, table, lens, q, causal=False, scale=0.3)
 
 
+@pytest.mark.parametrize("mode", ["nvfp4", "mxfp8"])
+@pytest.mark.parametrize("n", [1, 11])
+def test_scale_of_any_sign(nv, mode, n):
+    lens = [90, 33]
+    c, table = make(nv, mode, lens, 2, 64, 16, 13)
+    q = seeded((2 * n, 8, 64), 5, bf16)
+    for scale in (-0.2, 0.0):
+        compare(nv, c, table, lens, q, [0, n, 2 * n], n, scale=scale)
+
+
+@pytest.mark.parametrize("B", [32, 33, 75, 161, 500])
+@pytest.mark.parametrize("most,window", [(60, 0), (700, 100)])
+def test_many_sequences(nv, B, most, window):
+    """More sequences than a warp, or all of a CTA's, take at a time; some of
+    them empty, some without a query."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, most, (B,), generator=g).tolist()
+    lens[B // 2:B // 2 + 3] = [0, 0, 0]
+    n = torch.randint(0, 3, (B,), generator=g).clamp(max=torch.tensor(lens)).tolist()
+    n[0] = n[B - 1] = 1
+    starts = [0]
+    for x in n:
+        starts.append(starts[-1] + x)
+    c, table = make(nv, "nvfp4", lens, 2, 64, 16, 15)
+    q = seeded((starts[-1], 6, 64), 6, bf16)
+    compare(nv, c, table, lens, q, starts, 2, max(lens), window=window)
+    compare(nv, c, table, lens, seeded((B, 6, 64), 7, f16), workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("mode", ["nvfp4", "mxfp4", "mxfp8"])
 @pytest.mark.parametrize("dtype", [bf16, f16])
 @pytest.mark.parametrize("heads,G,D,page_size", [(2, 4, 128, 64), (3, 1, 96, 24), (1, 16, 64, 16), (2, 3, 256, 100),
