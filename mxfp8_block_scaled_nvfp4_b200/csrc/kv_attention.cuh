@@ -123,7 +123,7 @@ __device__ __forceinline__ float ex2(float x) {
 // 196 us, 4.66 TB/s or 71 % of the copy rate; 1 x 131072 46 us, of which 5 are
 // spent up to the first unit (lengths, page table, codes: three loads one
 // after the other) and 3 in the join.  Bound by memory and by the decoding
-// instructions (about 500 for 32 tokens a warp) alike.
+// instructions (660 for 32 tokens, the ALU pipe half busy) alike.
 //
 // Number formats.  NVFP4: code * block scale has six significant bits and
 // lies in [2^-10, 2688], so K_hat and V_hat are exact in fp16 (the global
