@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
   const uint32_t u0 = each * blockIdx.x + min(blockIdx.x, longer), u1 = u0 + each + (blockIdx.x < longer ? 1u : 0u);
   Cursor<ROWS, UNIT> at;
   at.b = a.B;
-  uint32_t found_at = 0, before = 0;  // units of the sequences before this round's
+  uint32_t found_at = 0, before = 0;  // units of the sequences before these
   for (uint32_t b0 = few ? 0u : 32u * warp;; b0 += ROUND) {
     const uint32_t v = few ? mine : units_of(b0 + lane);
     uint32_t incl = v;

@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         if (n + 1 < iters) {
           const uint32_t sn = (uint32_t)(n + 1) % S::st_k;
           if (t == 0 && !wait(full[0][sn], ((uint32_t)(n + 1) / S::st_k) & 1u)) break;
-          qk(t, n + 1);
+          qk(t, n + 1);  // behind P V in the thread's order: P is read before S takes its place
           if (t == nq - 1 && leader) mma_commit(smem_u32(&empty[0][sn]));
         }
         __syncwarp();
