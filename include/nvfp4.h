@@ -40,8 +40,8 @@
  *    checks happen on the host before anything is enqueued; on failure
  *    nothing is enqueued and nvfp4_last_error_message() explains.
  *    NVFP4_ERR_CUDA reports a launch error.  Device-side checks (an expert
- *    index out of range in gather_qmm; a bounded wait that gave up in the
- *    tensor-core GEMM) set a device error word instead of trapping; read it
+ *    index out of range in gather_qmm; a bounded wait that gave up in a
+ *    tensor-core GEMM or in kv_attention) set a device error word instead of trapping; read it
  *    with nvfp4_check_device_errors().
  *  - Empty outputs: a call whose output has no element (rows, N, M or T is
  *    0, or K is 0 for the quantizers) returns NVFP4_OK after its argument

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "kv_cache.cuh"
+#include "qqmm_sm100.cuh"
 
 namespace nvfp4 {
 namespace kv {
@@ -555,10 +556,12 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Waits with a hint of how long (in ns) the thread may be suspended; at most
-// 2^17 * 20 us.
-__device__ __forceinline__ bool wait_for(uint64_t& bar, uint32_t parity) {
-  for (uint32_t i = 0; i < (1u << 17); ++i) {
+// Waits with a hint of how long (in ns) the thread may be suspended; by
+// default at most 2^17 * 20 us.  A wait for what is still on its way into the
+// CTA's memory (kDrainPolls) keeps that limit in test builds too.
+constexpr uint32_t kPolls = tc::kWaitLimit / 512u, kDrainPolls = 1u << 17;
+__device__ __forceinline__ bool wait_for(uint64_t& bar, uint32_t parity, uint32_t polls = kPolls) {
+  for (uint32_t i = 0; i < polls; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -737,6 +740,10 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
           ok = false;
           break;
         }
+        if (tc::withheld_stage(it)) {
+          if (k + 1 < n) look(k + 1);
+          continue;
+        }
         const int32_t t0 = at.w.base + (int32_t)((at.off + k) * UNIT);
         const uint32_t bar = shared_u32(&full[st]), dst = shared_u32(stage_mem) + st * unit_bytes;
         if (run >= 16u) {
@@ -800,7 +807,8 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
     }
     if (!ok && lane == 0) abort_flag = 1;
     // what was asked for has landed before the CTA's memory goes
-    for (uint32_t i = it > (uint32_t)ST ? it - ST : 0; i < it; ++i) wait_for(full[i % ST], i / ST & 1u);
+    for (uint32_t i = it > (uint32_t)ST ? it - ST : 0; i < it; ++i)
+      if (!tc::withheld_stage(i)) wait_for(full[i % ST], i / ST & 1u, kDrainPolls);
     return;
   }
 

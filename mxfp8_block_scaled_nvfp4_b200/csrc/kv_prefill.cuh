@@ -237,9 +237,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
       : "r"(addr)
       : "memory");
 }
-// Barrier of the two warps that share 32 rows; a warp that gives up arrives
-// without waiting, after it has set the flag that its partner looks at before
-// every further wait.
+// Barrier of the two warps that share 32 rows.  A warp that gives up, wherever
+// it does, arrives once without waiting, after it has set abort_flag: its
+// partner may already be at the barrier or get there before it sees the flag,
+// and looks at the flag before it gets to the next one.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void pair_leave(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
 
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
                 tok, e0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive(smem_u32(&full[side][st]));
+      if (lane == 0 && !(side == 1 && warp == 0 && withheld_stage(n))) arrive(smem_u32(&full[side][st]));
       cur = next;
       next = fetch(q + 2);
     }
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     // every MMA issued here has completed before TMEM is released
     if (leader) mma_commit(smem_u32(&all_done));
     __syncwarp();
-    wait_for(all_done, 0);
+    wait_for(all_done, 0, kDrainPolls);
   } else if (softmax) {
     // ------------------------------------------------------------ softmax
     const uint32_t tl = tmem + ((32u * ((uint32_t)warp & 3u)) << 16);
@@ -615,12 +616,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       if (lane == 0) arrive(smem_u32(&p_full[qt]));
     }
     if (ok && iters > 0) {
-      ok = __all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(iters - 1) & 1u) && !abort_flag);
+      if (!__all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(iters - 1) & 1u) && !abort_flag)) ok = leave();
       tc_fence_after();
     }
-    if (!ok) {
-      if (lane == 0) abort_flag = 1;
-    } else {
+    if (ok) {
       // the row's sum (the slots were last read before the last P)
       other[qt][half][row] = l;
       pair_sync(2 + 4 * qt + (warp & 3));

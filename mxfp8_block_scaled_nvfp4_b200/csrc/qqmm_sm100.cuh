@@ -90,7 +90,9 @@ constexpr uint32_t kWaitLimit = NVFP4_WAIT_LIMIT;
 // issues neither the arrival nor any copy of its stage s, so the MMA warp's
 // bounded wait on that stage runs out and the kernel takes its timeout path
 // (error word, drain, TMEM freed).  No copy is left in flight: nothing is
-// issued for the withheld stage.  The library itself is built without it.
+// issued for the withheld stage.  In the attention kernels over the key/value
+// cache CTA 0's copy warp skips unit s, or one producer warp does not arrive
+// for value tile s.  The library itself is built without it.
 __device__ __forceinline__ bool withheld_stage(uint32_t it) {
 #ifdef NVFP4_TEST_WITHHOLD_STAGE
   return blockIdx.x == 0 && it == (uint32_t)(NVFP4_TEST_WITHHOLD_STAGE);
