@@ -446,7 +446,8 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  *   lse = ln(sum_j exp(z_j)),
  * with k_hat, v_hat the cache's exact values (code * block scale * g/2688;
  * not rounded to q's type), fp32 sums and statistics.  A query that sees
- * nothing gets out = 0 and lse = -infinity.  Query head h reads key/value
+ * nothing gets out = 0 and lse = -infinity.  A NaN in a query makes its own
+ * out and lse NaN, and no others.  Query head h reads key/value
  * head h / (Hq / heads).
  * q: fp16 or bf16, [T, Hq, D], heads and D contiguous, tokens q_stride
  * elements apart (>= Hq*D, or any value for T <= 1; a multiple of 16 bytes).

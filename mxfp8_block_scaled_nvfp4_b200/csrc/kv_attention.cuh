@@ -86,6 +86,10 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& a, const Seq& s, uin
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// ln of a row's sum; a row that saw nothing has l = 0, one with a NaN logit
+// (a NaN in its query) l = NaN.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
 // 2^k, -126 <= k <= 127.
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
@@ -1001,10 +1005,10 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
       }
       const uint32_t i = r / a.G, h = at.hk * a.G + (r - i * a.G);
       const uint64_t to = (uint64_t)(s.t0 + i) * a.Hq + h;
-      const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
+      const float f = whole ? (l == 0.0f ? 0.0f : fv / l) : fv;
       if (d.g == 0 && k == 0) {
         if (!whole) a.part_ml[slot * ROWS + lr] = make_float2(M, l);
-        else if (a.lse) a.lse[to] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
+        else if (a.lse) a.lse[to] = lse_of(M, l);
       }
       float v[8];
 #pragma unroll
@@ -1080,9 +1084,9 @@ __global__ void __launch_bounds__(256) k_kv_decode_join(const __grid_constant__ 
   l = sl[w0] + sl[w0 + 1] + sl[w0 + 2] + sl[w0 + 3];
   const uint32_t x = (uint32_t)more.x + lr, i = x / a.G;  // query after the tile's first, head of the group
   const uint64_t at = (uint64_t)((uint32_t)head.z + i) * a.Hq + (uint32_t)more.y * a.G + (x - i * a.G);
-  if (a.lse && lane == 0) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[at] = lse_of(m, l);
   if (d0 >= a.D) return;
-  const float f = l > 0.0f ? 1.0f / l : 0.0f;
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = (so[w0][d0 + e] + so[w0 + 1][d0 + e] + so[w0 + 2][d0 + e] + so[w0 + 3][d0 + e]) * f;
   store8<QT>(static_cast<QT*>(a.out) + at * a.D + d0, o);
@@ -1133,14 +1137,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_consta
   if (warp != 0) return;
   l = 0.0f;
   for (int w = 0; w < kJoinWarps; ++w) l += sl[w];
-  if (a.lse && lane == 0) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[at] = lse_of(m, l);
   if (d0 >= a.D) return;
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     v[e] = 0.0f;
     for (int w = 0; w < kJoinWarps; ++w) v[e] += so[w][d0 + e];
-    v[e] = l > 0.0f ? v[e] / l : 0.0f;
+    v[e] = l == 0.0f ? 0.0f : v[e] / l;
   }
   store8<QT>(static_cast<QT*>(a.out) + at * a.D + d0, v);
 }

@@ -627,10 +627,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       const uint32_t h = hk * a.G + (min(r, R - 1u) - i * a.G);
       const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
       const float fv = kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
-      const float f = whole ? (l > 0.0f ? fv / l : 0.0f) : fv;
+      const float f = whole ? (l == 0.0f ? 0.0f : fv / l) : fv;
       if (r < R && half == 0) {
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);
-        else if (a.lse) a.lse[at] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        else if (a.lse) a.lse[at] = lse_of(m, l);
       }
       for (uint32_t c = 16u * half; c < a.D; c += 32u) {
         uint32_t y[16];
