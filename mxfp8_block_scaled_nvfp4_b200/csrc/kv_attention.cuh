@@ -90,6 +90,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // (a NaN in its query) l = NaN.
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
+// The weights are kept times 2^kUp, so that their 16-bit terms (and, in the MX
+// modes, the products with values that are held times 2^-64) keep their bits.
+// Below 2^8 times that: fp16 ends at 2^16.
+template <int MODE>
+constexpr float kUp = MODE == kNV ? 7.0f : 32.0f;
+
 // 2^k, -126 <= k <= 127.
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
@@ -134,8 +140,12 @@ __device__ __forceinline__ float ex2(float x) {
 // lies in [2^-10, 2688], so K_hat and V_hat are exact in fp16 (the global
 // scales are factors of the logits and of the output).  A query row is scaled
 // by a power of two to [2^14, 2^15) and rounds to fp16 exactly (elements
-// 2^-28 below the row's largest lose bits that fp32 sums lose too); P is
-// rounded to fp16 (2^-11 relative; the weights sum in fp32 unrounded).
+// 2^-28 below the row's largest lose bits that fp32 sums lose too).  P, times
+// 2^7, is rounded to fp16: 16 bits are what one product per code takes, and
+// bf16 or fp16 outputs have no more.  That is 2^-11 relative down to weights
+// of 2^-21 of the reference, then half a step of fp16's subnormals, 2^-32 of
+// it (2^-25 without the factor: 131072 tokens that light beside a heavy one
+// lost 2^-8 of the output).  The weights sum in fp32 unrounded.
 // MX modes: code * 2^e spans fp32's exponents, so K_hat and V_hat are bf16
 // (exact: at most four significant bits) times 2^-64; a query row is scaled
 // to [2^40, 2^41) and split into two bf16 terms when it is fp16 (11 bits = 8
@@ -886,7 +896,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
         }
       }
       // The running maximum moves only when a step exceeds it by 2^8 (weights
-      // then lie below 2^8, which fp16 and the sums hold as well as below 1).
+      // then lie below 2^(8 + kUp), which 16 bits and the sums hold).
       float top[NT][2];
       bool grow = false;
 #pragma unroll
@@ -899,7 +909,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          top[nt][e] = x * d.fz[nt][e] - (D::kMx ? 32.0f : 0.0f);
+          top[nt][e] = x * d.fz[nt][e] - kUp<MODE>;
           grow = grow || top[nt][e] > d.m[nt][e] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grow)) {

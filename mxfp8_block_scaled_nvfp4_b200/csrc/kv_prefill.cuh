@@ -31,7 +31,7 @@
 // and the next S bounds it.  Tiles of 64 tokens with two S buffers hid more of
 // the chain, but an N = 64 product takes as long as an N = 128 one (671 us).
 //
-// Number formats as in k_kv_decode: NVFP4 exact fp16 operands, P in fp16; MX
+// Number formats as in k_kv_decode: NVFP4 exact fp16 operands, P times 2^7 in fp16; MX
 // modes exact bf16 operands times 2^-64 and P in two bf16 terms, each with
 // its own MMA.  (fp16 queries over an MX cache would need two terms of Q as
 // well; they stay with k_kv_decode.)
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       // (its slot was read before the P that this S followed)
       other[qt][half][row] = top;
       pair_sync(2 + 4 * qt + (warp & 3));
-      top = fmaxf(top, other[qt][half ^ 1][row]) * fz - (kMx ? 32.0f : 0.0f);
+      top = fmaxf(top, other[qt][half ^ 1][row]) * fz - kUp<MODE>;
       tmem_ld32_wait(x);
       // the reference moves only when exceeded by 2^8 (see k_kv_decode)
       if (__any_sync(0xffffffffu, top > m + 8.0f)) {

@@ -41,3 +41,46 @@ def test_a_nan_query_gives_nan_and_leaves_the_others(nv, mode, dtype, n, L):
             assert torch.isfinite(out[rest].float()).all() and torch.isfinite(lse[rest]).all()
             if not kw:
                 assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("n", [1, 10])
+@pytest.mark.parametrize("power", [20.0, 25.7, 27.0])
+def test_many_light_tokens_beside_heavy_ones(nv, mode, dtype, n, power):
+    """131072 tokens of weight 2^-power beside four of weight 1 whose values are
+    zero: all of the output comes from weights far below the largest.
+
+    Tolerance, relative to the largest weight 1.  The kernels hold weights as
+    16-bit floats times at least 2^7 (fp16: half a step of its subnormals is
+    2^-25, so 2^-32 a weight) or in two bf16 terms (2^-16 relative): with
+    A = sum w |v| = out, sum w = l,
+      u out + (2^-11 + 2 dz + sums) A + 2^-32 sum |v| / l.
+    The logits of the light tokens are 0 and exact but for the reference's
+    2^-22 * power ln 2."""
+    D, L, page = 64, 131072, 1024
+    g = [torch.tensor([2688.0], device="cuda")] * 2 if mode == "nvfp4" else [None] * 2
+    c = nv.KvCache.empty(mode, L // page, 1, page, D, *g)
+    k, v = torch.zeros(L, 1, D, dtype=bf16, device="cuda"), torch.full((L, 1, D), 6.0, dtype=bf16, device="cuda")
+    heavy = torch.tensor([0, 32, 64, 96], device="cuda")  # one for each warp of a CTA
+    k[heavy, :, 0] = 6.0
+    v[heavy] = 0.0
+    nv.kv_cache_write(c, k, v, torch.arange(L, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(n, 4, D, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    scale = power * math.log(2.0) / 6.0
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda")[None]
+    ko, vo = nv.kv_cache_read(c, i32([0, 1]), torch.float32)
+    assert ko[0, 0, 0] == 6 and ko[1].abs().sum() == 0 and vo[0].abs().sum() == 0 and (vo[1] == 6).all()
+    light = 2.0 ** (-scale * 6.0 / math.log(2.0))
+    l = 4 + (L - 4) * light
+    want, total = (L - 4) * light * 6.0 / l, math.log(l) + scale * 6.0
+    dz = 2.0 ** -21 * scale * 6.0 + 2.0 ** -22
+    sums = (L / 4 + 160) * 2.0 ** -23
+    tol = torch.finfo(dtype).eps / 2 * want + (2.0 ** -11 + 2 * dz + sums) * want + 2.0 ** -32 * L * 6.0 / l
+    assert tol < want / 20
+    for kw in ({}, {"workspace": no_workspace()}):
+        out, lse = nv.kv_attention(c, q, table, i32([L]), i32([0, n]), n, L, scale=scale, causal=False, return_lse=True, **kw)
+        nv.check_device_errors()
+        assert ((out.double() - want).abs() <= tol).all(), (out.double().min(), out.double().max(), want, tol)
+        assert ((lse.double() - total).abs() <= dz + 2.0 ** -22 * total + sums).all()
