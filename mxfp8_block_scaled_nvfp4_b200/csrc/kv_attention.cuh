@@ -91,10 +91,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
 // The weights are kept times 2^kUp, so that their 16-bit terms (and, in the MX
-// modes, the products with values that are held times 2^-64) keep their bits.
-// Below 2^8 times that: fp16 ends at 2^16.
+// modes, the products with very small values) keep their bits.  They reach 2^8
+// times that, which fp16 (2^16) and the sums over 2^30 tokens of values below
+// 2^73 (2^128) have to hold.
 template <int MODE>
-constexpr float kUp = MODE == kNV ? 7.0f : 32.0f;
+constexpr float kUp = MODE == kNV ? 7.0f : 16.0f;
 
 // 2^k, -126 <= k <= 127.
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
@@ -147,10 +148,12 @@ __device__ __forceinline__ float ex2(float x) {
 // it (2^-25 without the factor: 131072 tokens that light beside a heavy one
 // lost 2^-8 of the output).  The weights sum in fp32 unrounded.
 // MX modes: code * 2^e spans fp32's exponents, so K_hat and V_hat are bf16
-// (exact: at most four significant bits) times 2^-64; a query row is scaled
-// to [2^40, 2^41) and split into two bf16 terms when it is fp16 (11 bits = 8
-// + 3), and P, scaled by 2^32, into two bf16 terms (16 bits), so nothing
-// rounds to fewer bits than fp16 would.
+// (exact: at most four significant bits; bf16's subnormals end at 2^-133, so
+// MXFP8 blocks with a scale below 2^-124 round to multiples of that).  A query
+// row is scaled to [2^16, 2^17) and split into two bf16 terms when it is fp16
+// (11 bits = 8 + 3), and P, times 2^16, into two bf16 terms (16 bits), so
+// nothing rounds to fewer bits than fp16 would.  With scales of at most 2^64
+// and 2^30 tokens every sum stays below 2^127.
 enum { kDecWarps = 4, kDecThreads = (kDecWarps + 1) * 32 };
 
 template <int MODE, int DP>
@@ -225,13 +228,18 @@ __device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w) {
   const uint32_t mg = I == 0 ? w << 4 : w >> 4;
   return (sg & 0x80008000u) | (mg & 0x07F007F0u);
 }
-// bf16 of 2^(s - 127 - 64 + up) for an e8m0 byte s (capped at 2^64), `up` the
-// power of two that the pair functions above leave out (126 or 120): exponent
-// field min(s, 191) - 64 + up, at most 253.
-template <int MODE>
-__device__ __forceinline__ uint32_t mx_factor(uint32_t s) {
-  return (min(s, 191u) + (MODE == kMX8 ? 56u : 62u)) << 7;
+// Two MXFP4 codes (nibbles i and i + 4 of a word) or two MXFP8 codes (bytes i
+// and i + 2) times the pair f of block scales.  The power of two that the pair
+// functions above leave out and the block scale are two products: as one
+// factor, 2^254 at the most, they are beyond bf16, and a smaller one loses
+// small blocks.
+template <int MODE, int I>
+__device__ __forceinline__ uint32_t mx_pair(uint32_t w, uint32_t f) {
+  if constexpr (MODE == kMX8) return mul_bf16x2(mul_bf16x2(e4m3_pair_bf16<I>(w), 0x7B807B80u), f);
+  else return mul_bf16x2(mul_bf16x2(e2m1_pair_bf16<I>(w), 0x7E807E80u), f);
 }
+// bf16 of 2^(s - 127) for an e8m0 byte s, capped at 2^64; s = 0 is a subnormal.
+__device__ __forceinline__ uint32_t mx_factor(uint32_t s) { return max(min(s, 191u) << 7, 0x40u); }
 
 template <int BYTES>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -307,7 +315,7 @@ struct Decode {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // 2^e <= mx < 2^(e+1), kept where every factor below is normal
       const int e = mx > 0.0f ? max(-80, (int)((__float_as_uint(mx) >> 23) & 255u) - 127) : 0;
-      constexpr int top = kMx ? 40 : 14;
+      constexpr int top = kMx ? 16 : 14;
       const float up = pow2(top - e) * (a.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
       for (int s = 0; s < G::ksteps; ++s)
@@ -324,7 +332,7 @@ struct Decode {
           }
         }
       // row 8 nt + g's factor, wanted by the lanes of columns 2c, 2c + 1
-      const float f = fmaxf(fabsf(a.scale) * kLog2e * pow2(e) * gk * pow2(kMx ? 24 : -14), 1e-37f);
+      const float f = fmaxf(fabsf(a.scale) * kLog2e * pow2(e) * gk * pow2(-top), 1e-37f);
       fz[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
       fz[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
     }
@@ -422,18 +430,18 @@ struct Decode {
         if (w % wpb == 0)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            f[i] = mx_factor<MODE>((ks[i] >> (8 * (w / wpb))) & 255u);
+            f[i] = mx_factor((ks[i] >> (8 * (w / wpb))) & 255u);
             f[i] |= f[i] << 16;
           }
         const uint32_t a = kw[0][w], b = kw[1][w];
         if constexpr (MODE == kMX4) {
-          step_mma(s, 2 * w, mul_bf16x2(e2m1_pair_bf16<0>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<0>(b), f[1]),
-                   mul_bf16x2(e2m1_pair_bf16<1>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<1>(b), f[1]));
-          step_mma(s, 2 * w + 1, mul_bf16x2(e2m1_pair_bf16<2>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<2>(b), f[1]),
-                   mul_bf16x2(e2m1_pair_bf16<3>(a), f[0]), mul_bf16x2(e2m1_pair_bf16<3>(b), f[1]));
+          step_mma(s, 2 * w, mx_pair<MODE, 0>(a, f[0]), mx_pair<MODE, 0>(b, f[1]),
+                   mx_pair<MODE, 1>(a, f[0]), mx_pair<MODE, 1>(b, f[1]));
+          step_mma(s, 2 * w + 1, mx_pair<MODE, 2>(a, f[0]), mx_pair<MODE, 2>(b, f[1]),
+                   mx_pair<MODE, 3>(a, f[0]), mx_pair<MODE, 3>(b, f[1]));
         } else {
-          step_mma(s, w, mul_bf16x2(e4m3_pair_bf16<0>(a), f[0]), mul_bf16x2(e4m3_pair_bf16<0>(b), f[1]),
-                   mul_bf16x2(e4m3_pair_bf16<1>(a), f[0]), mul_bf16x2(e4m3_pair_bf16<1>(b), f[1]));
+          step_mma(s, w, mx_pair<MODE, 0>(a, f[0]), mx_pair<MODE, 0>(b, f[1]),
+                   mx_pair<MODE, 1>(a, f[0]), mx_pair<MODE, 1>(b, f[1]));
         }
       }
     }
@@ -484,8 +492,8 @@ struct Decode {
                   mul_f16x2(y23[e], s23), ph, pl);
       }
     } else {
-      const uint32_t f01 = mx_factor<MODE>(vs[0]) | (mx_factor<MODE>(vs[1]) << 16);
-      const uint32_t f23 = mx_factor<MODE>(vs[2]) | (mx_factor<MODE>(vs[3]) << 16);
+      const uint32_t f01 = mx_factor(vs[0]) | (mx_factor(vs[1]) << 16);
+      const uint32_t f23 = mx_factor(vs[2]) | (mx_factor(vs[3]) << 16);
 #pragma unroll
       for (int w = 0; w < G::vw; ++w)
 #pragma unroll
@@ -493,13 +501,13 @@ struct Decode {
           const uint32_t sel = hf ? 0x7632u : 0x5410u;
           const uint32_t u = __byte_perm(vw[0][w], vw[1][w], sel), v = __byte_perm(vw[2][w], vw[3][w], sel);
           if constexpr (MODE == kMX4) {
-            out_mma(4 * w + 2 * hf, mul_bf16x2(e2m1_pair_bf16<0>(u), f01), mul_bf16x2(e2m1_pair_bf16<1>(u), f01),
-                    mul_bf16x2(e2m1_pair_bf16<0>(v), f23), mul_bf16x2(e2m1_pair_bf16<1>(v), f23), ph, pl);
-            out_mma(4 * w + 2 * hf + 1, mul_bf16x2(e2m1_pair_bf16<2>(u), f01), mul_bf16x2(e2m1_pair_bf16<3>(u), f01),
-                    mul_bf16x2(e2m1_pair_bf16<2>(v), f23), mul_bf16x2(e2m1_pair_bf16<3>(v), f23), ph, pl);
+            out_mma(4 * w + 2 * hf, mx_pair<MODE, 0>(u, f01), mx_pair<MODE, 1>(u, f01),
+                    mx_pair<MODE, 0>(v, f23), mx_pair<MODE, 1>(v, f23), ph, pl);
+            out_mma(4 * w + 2 * hf + 1, mx_pair<MODE, 2>(u, f01), mx_pair<MODE, 3>(u, f01),
+                    mx_pair<MODE, 2>(v, f23), mx_pair<MODE, 3>(v, f23), ph, pl);
           } else {
-            out_mma(2 * w + hf, mul_bf16x2(e4m3_pair_bf16<0>(u), f01), mul_bf16x2(e4m3_pair_bf16<1>(u), f01),
-                    mul_bf16x2(e4m3_pair_bf16<0>(v), f23), mul_bf16x2(e4m3_pair_bf16<1>(v), f23), ph, pl);
+            out_mma(2 * w + hf, mx_pair<MODE, 0>(u, f01), mx_pair<MODE, 1>(u, f01),
+                    mx_pair<MODE, 0>(v, f23), mx_pair<MODE, 1>(v, f23), ph, pl);
           }
         }
     }
@@ -1001,7 +1009,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
     sync();
     // eight elements (m-tiles 4k .. 4k + 3) of the lane's columns 2c + e of n-tile nt
     const uint32_t slot = 2u * blockIdx.x + (seg ? 1u : 0u);
-    const float fv = D::kMx ? 0x1p64f : gv;
+    const float fv = D::kMx ? 1.0f : gv;
 #pragma unroll 1
     for (uint32_t item = warp; item < NT * (DP / 64) * 2u; item += kDecWarps) {
       const uint32_t e = item & 1u, k = (item >> 1) % (DP / 64), nt = (item >> 1) / (DP / 64);

@@ -32,7 +32,7 @@
 // the chain, but an N = 64 product takes as long as an N = 128 one (671 us).
 //
 // Number formats as in k_kv_decode: NVFP4 exact fp16 operands, P times 2^7 in fp16; MX
-// modes exact bf16 operands times 2^-64 and P in two bf16 terms, each with
+// modes exact bf16 operands and P in two bf16 terms, each with
 // its own MMA.  (fp16 queries over an MX cache would need two terms of Q as
 // well; they stay with k_kv_decode.)
 #pragma once
@@ -133,11 +133,11 @@ __device__ __forceinline__ uint4 decode8(const uint32_t* w, uint32_t f) {
     e2m1x8_to_f16x2(w[0], v);
     return make_uint4(mul_f16x2(v[0], f), mul_f16x2(v[1], f), mul_f16x2(v[2], f), mul_f16x2(v[3], f));
   } else if constexpr (MODE == kMX4) {
-    return make_uint4(mul_bf16x2(e2m1_pair_bf16<0>(w[0]), f), mul_bf16x2(e2m1_pair_bf16<1>(w[0]), f),
-                      mul_bf16x2(e2m1_pair_bf16<2>(w[0]), f), mul_bf16x2(e2m1_pair_bf16<3>(w[0]), f));
+    return make_uint4(mx_pair<MODE, 0>(w[0], f), mx_pair<MODE, 1>(w[0], f),
+                      mx_pair<MODE, 2>(w[0], f), mx_pair<MODE, 3>(w[0], f));
   } else {
-    return make_uint4(mul_bf16x2(e4m3_pair_bf16<0>(w[0]), f), mul_bf16x2(e4m3_pair_bf16<1>(w[0]), f),
-                      mul_bf16x2(e4m3_pair_bf16<0>(w[1]), f), mul_bf16x2(e4m3_pair_bf16<1>(w[1]), f));
+    return make_uint4(mx_pair<MODE, 0>(w[0], f), mx_pair<MODE, 1>(w[0], f),
+                      mx_pair<MODE, 0>(w[1], f), mx_pair<MODE, 1>(w[1], f));
   }
 }
 
@@ -195,7 +195,7 @@ struct Raw {
         f[0] = __byte_perm(pr, 0, 0x1010);
         f[1] = __byte_perm(pr, 0, 0x3232);
       } else {
-        const uint32_t q = mx_factor<MODE>((sc >> (8 * u)) & 255u);
+        const uint32_t q = mx_factor((sc >> (8 * u)) & 255u);
         f[0] = f[1] = q | (q << 16);
       }
 #pragma unroll
@@ -350,9 +350,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
     }
     const int e2 = mx > 0.0f ? max(-80, (int)((__float_as_uint(mx) >> 23) & 255u) - 127) : 0;
-    const float up = pow2((kMx ? 40 : 14) - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
+    constexpr int up2 = kMx ? 16 : 14;
+    const float up = pow2(up2 - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
     const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
-    fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(kMx ? 24 : -14), 1e-37f);
+    fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(-up2), 1e-37f);
     for (uint32_t o = half; o < a.D / 8u; o += 2u) {
       float x[8];
       load8<QT>(q + 8u * o, x);
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       l += other[qt][half ^ 1][row];
       const uint32_t h = hk * a.G + (min(r, R - 1u) - i * a.G);
       const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
-      const float fv = kMx ? 0x1p64f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
+      const float fv = kMx ? 1.0f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
       const float f = whole ? (l == 0.0f ? 0.0f : fv / l) : fv;
       if (r < R && half == 0) {
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);

@@ -84,3 +84,57 @@ def test_many_light_tokens_beside_heavy_ones(nv, mode, dtype, n, power):
         nv.check_device_errors()
         assert ((out.double() - want).abs() <= tol).all(), (out.double().min(), out.double().max(), want, tol)
         assert ((lse.double() - total).abs() <= dz + 2.0 ** -22 * total + sums).all()
+
+
+@pytest.mark.parametrize("mode", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("kexp,vexp", [(-70, (-64, -70, -76, -84)), (-100, (-100, -110, -118, 0)), (50, (60, 58, -118, 0))])
+def test_mx_blocks_far_from_one(nv, mode, dtype, n, kexp, vexp):
+    """Value blocks of the given powers of two beside one another, keys of
+    2^kexp with a scale that brings the logits back to order one."""
+    L, D = 300, 128
+    c, table = make(nv, mode, [L], 1, D, 16, 47)
+    j = torch.arange(L)
+    slots = (table[0].cpu()[j // 16] * 16 + j % 16).to(torch.int32).cuda()
+    k = seeded((L, 1, D), 1, torch.float32) * 2.0 ** kexp
+    v = seeded((L, 1, D), 2, torch.float32)
+    v = (v.unflatten(-1, (-1, 32)) * torch.exp2(torch.tensor([float(x) for x in vexp], device="cuda"))[:, None]).flatten(-2)
+    nv.kv_cache_write(c, k.contiguous(), v.contiguous(), slots)
+    q = seeded((n, 4, D), 3, dtype)
+    scale = D ** -0.5 * 2.0 ** -kexp
+    out, lse = torch.empty_like(q, dtype=dtype), torch.empty(n, 4, device="cuda")
+    for kw in ({}, {"workspace": no_workspace()}):
+        nv.kv_attention(c, q, table, i32([L]), i32([0, n]), n, L, scale=scale, out=out, lse=lse, **kw)
+        nv.check_device_errors()
+        o, l, tol, ltol = attention(cache_sides(c), q, table, torch.tensor([L]), torch.tensor([0, n]), scale)
+        lost = o.abs() > torch.finfo(dtype).max  # beyond fp16
+        assert torch.isinf(out.cpu()[lost]).all()
+        o[lost] = float("nan")
+        check(out, o, tol, "out")
+        check(lse, l, ltol, "lse")
+        if dtype == bf16:
+            assert (out.abs().amax((0, 1)).view(4, 32) > 0).all()
+
+
+@pytest.mark.parametrize("mode", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_mx_largest_values_over_a_long_range(nv, mode, n):
+    """Values of 2^64 times the largest code, equal weights after a rise of the
+    logits that the running maximum does not follow (less than 2^8)."""
+    D, L, page = 32, 1 << 17, 1024
+    c = nv.KvCache.empty(mode, L // page, 1, page, D)
+    most = {"mxfp4": 6.0, "mxfp8": 448.0}[mode]
+    k = torch.ones(L, 1, D, dtype=bf16, device="cuda")
+    k[:256] = 0
+    v = torch.full((L, 1, D), most * 2.0 ** 64, dtype=bf16, device="cuda")
+    nv.kv_cache_write(c, k, v, torch.arange(L, dtype=torch.int32, device="cuda"))
+    assert (nv.kv_cache_read(c, i32([5]))[1] == most * 2.0 ** 64).all()
+    q = torch.ones(n, 1, D, dtype=bf16, device="cuda")
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda")[None]
+    for kw in ({}, {"workspace": no_workspace()}):
+        out = nv.kv_attention(c, q, table, i32([L]), i32([0, n]), n, L, scale=7.0 * math.log(2.0) / D, causal=False, **kw)
+        nv.check_device_errors()
+        # half a bf16 step, the weights' 2^-16 and the fp32 sums of 2^17 terms in four chains
+        tol = 2.0 ** -9 + 2.0 ** -16 + (L / 4 + 160) * 2.0 ** -23
+        assert ((out.double() / (most * 2.0 ** 64) - 1).abs() <= tol).all()
