@@ -463,9 +463,9 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  * A sequence whose entries break these bounds is skipped (its rows left as
  * they are), and a token on a page out of range counts as unseen; both set
  * NVFP4_ERR_DEVICE_INDEX.
- * MX modes: a block scale above 2^64 (0xFF included) counts as 2^64; MXFP8
- * values under a block scale below 2^-124 count as the nearest multiples of
- * 2^-133.
+ * MX modes: a block scale above 2^64 (0xFF included) counts as 2^64, and
+ * elements that are no multiples of 2^-133 (MXFP4 keys: of 2^-109) count as
+ * the nearest one.
  * Hq a multiple of heads, Hq <= 65535; B <= 65535; T*Hq*D at most 2^34;
  * B*heads*ceil(max_q*(Hq/heads)/8)*(max_kv/64 + 2) below 2^32.
  * workspace: device scratch, 16-byte aligned, contents undefined on entry

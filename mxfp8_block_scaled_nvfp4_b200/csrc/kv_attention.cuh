@@ -149,7 +149,7 @@ __device__ __forceinline__ float ex2(float x) {
 // lost 2^-8 of the output).  The weights sum in fp32 unrounded.
 // MX modes: code * 2^e spans fp32's exponents, so K_hat and V_hat are bf16
 // (exact: at most four significant bits; bf16's subnormals end at 2^-133, so
-// MXFP8 blocks with a scale below 2^-124 round to multiples of that).  A query
+// elements below that, MXFP4 keys below 2^-109, round to multiples of it).  A query
 // row is scaled to [2^16, 2^17) and split into two bf16 terms when it is fp16
 // (11 bits = 8 + 3), and P, times 2^16, into two bf16 terms (16 bits), so
 // nothing rounds to fewer bits than fp16 would.  With scales of at most 2^64
@@ -228,18 +228,37 @@ __device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w) {
   const uint32_t mg = I == 0 ? w << 4 : w >> 4;
   return (sg & 0x80008000u) | (mg & 0x07F007F0u);
 }
-// Two MXFP4 codes (nibbles i and i + 4 of a word) or two MXFP8 codes (bytes i
-// and i + 2) times the pair f of block scales.  The power of two that the pair
-// functions above leave out and the block scale are two products: as one
-// factor, 2^254 at the most, they are beyond bf16, and a smaller one loses
-// small blocks.
-template <int MODE, int I>
-__device__ __forceinline__ uint32_t mx_pair(uint32_t w, uint32_t f) {
-  if constexpr (MODE == kMX8) return mul_bf16x2(mul_bf16x2(e4m3_pair_bf16<I>(w), 0x7B807B80u), f);
-  else return mul_bf16x2(mul_bf16x2(e2m1_pair_bf16<I>(w), 0x7E807E80u), f);
+// MX values take the power of two that the pair functions leave out (2^126,
+// 2^120) and the block scale 2^(s - 127), s an e8m0 byte capped at 2^64.  As one
+// factor they are a bf16 number up to a scale of 2 (MXFP4) or 2^7 (MXFP8); a
+// smaller factor for all would lose small blocks.  So they are two products,
+// but for MXFP4 tiles without a larger scale (not BIG): 16 x 8192 tokens 49.2 us
+// where two products everywhere take 52.0.  MXFP4 keys, which outlying channels
+// put above that, are held times 2^-24, so that 2^25 is their border.  MXFP8
+// gains nothing (8 x 6000 of D 256: 64.8 us with the choice, 55.3 without).
+template <int MODE>
+struct Mx {
+  static constexpr uint32_t left_out = MODE == kMX8 ? 120 : 126;
+  static constexpr int key_down = MODE == kMX4 ? 24 : 0;  // keys are held times 2^-key_down
+  // of a key or a value
+  __device__ static constexpr uint32_t up(bool key) { return left_out - (key ? key_down : 0); }
+  __device__ static constexpr uint32_t largest(bool key) { return 254u - up(key); }  // scale byte that one factor holds
+};
+// The factor of a block, to be multiplied with pairs after `first`.
+template <bool BIG>
+__device__ __forceinline__ uint32_t mx_factor(uint32_t s, uint32_t up) {
+  return BIG ? max(min(s, 191u) << 7, 0x40u) : (s + up) << 7;
 }
-// bf16 of 2^(s - 127) for an e8m0 byte s, capped at 2^64; s = 0 is a subnormal.
-__device__ __forceinline__ uint32_t mx_factor(uint32_t s) { return max(min(s, 191u) << 7, 0x40u); }
+// Nibbles i and i + 4 (MXFP4) or bytes i and i + 2 (MXFP8) of a word times the
+// pair f of factors.
+template <int MODE, int I, bool BIG>
+__device__ __forceinline__ uint32_t mx_pair(uint32_t w, uint32_t f, uint32_t up) {
+  uint32_t p;
+  if constexpr (MODE == kMX8) p = e4m3_pair_bf16<I>(w);
+  else p = e2m1_pair_bf16<I>(w);
+  if constexpr (BIG) p = mul_bf16x2(p, (up + 127u) * 0x00800080u);
+  return mul_bf16x2(p, f);
+}
 
 template <int BYTES>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -332,7 +351,7 @@ struct Decode {
           }
         }
       // row 8 nt + g's factor, wanted by the lanes of columns 2c, 2c + 1
-      const float f = fmaxf(fabsf(a.scale) * kLog2e * pow2(e) * gk * pow2(-top), 1e-37f);
+      const float f = fmaxf(fabsf(a.scale) * kLog2e * pow2(e) * gk * pow2(Mx<MODE>::key_down - top), 1e-37f);
       fz[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
       fz[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
     }
@@ -422,27 +441,37 @@ struct Decode {
         step_mma(s, 2 * w, x[0], y[0], x[1], y[1]);
         step_mma(s, 2 * w + 1, x[2], y[2], x[3], y[3]);
       }
+    } else if constexpr (MODE == kMX4) {
+      uint32_t most = max(ks[0] & 255u, ks[1] & 255u);
+      if constexpr (DP == 256) most = max(most, max(ks[0] >> 8, ks[1] >> 8));
+      if (__any_sync(0xffffffffu, most > Mx<MODE>::largest(true))) mx_logits<true>(kw, ks, s);
+      else mx_logits<false>(kw, ks, s);
     } else {
-      constexpr int wpb = 32 * (int)Fmt<MODE>::bits / 32;  // words a block
-      uint32_t f[2] = {0, 0};
+      mx_logits<true>(kw, ks, s);
+    }
+  }
+
+  template <bool BIG>
+  __device__ __forceinline__ void mx_logits(const uint32_t (&kw)[2][G::kw], const uint32_t (&ks)[2], float (&s)[NT][4]) {
+    constexpr uint32_t up = Mx<MODE>::up(true);
+    constexpr int wpb = 32 * (int)Fmt<MODE>::bits / 32;  // words a block
+    uint32_t f[2] = {0, 0};
 #pragma unroll
-      for (int w = 0; w < G::kw; ++w) {
-        if (w % wpb == 0)
+    for (int w = 0; w < G::kw; ++w) {
+      if (w % wpb == 0)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            f[i] = mx_factor((ks[i] >> (8 * (w / wpb))) & 255u);
-            f[i] |= f[i] << 16;
-          }
-        const uint32_t a = kw[0][w], b = kw[1][w];
-        if constexpr (MODE == kMX4) {
-          step_mma(s, 2 * w, mx_pair<MODE, 0>(a, f[0]), mx_pair<MODE, 0>(b, f[1]),
-                   mx_pair<MODE, 1>(a, f[0]), mx_pair<MODE, 1>(b, f[1]));
-          step_mma(s, 2 * w + 1, mx_pair<MODE, 2>(a, f[0]), mx_pair<MODE, 2>(b, f[1]),
-                   mx_pair<MODE, 3>(a, f[0]), mx_pair<MODE, 3>(b, f[1]));
-        } else {
-          step_mma(s, w, mx_pair<MODE, 0>(a, f[0]), mx_pair<MODE, 0>(b, f[1]),
-                   mx_pair<MODE, 1>(a, f[0]), mx_pair<MODE, 1>(b, f[1]));
-        }
+        for (int i = 0; i < 2; ++i) f[i] = mx_factor<BIG>((ks[i] >> (8 * (w / wpb))) & 255u, up) * 0x10001u;
+      const uint32_t a = kw[0][w], b = kw[1][w];
+      auto k = [&](auto i, uint32_t x, uint32_t by) { return mx_pair<MODE, decltype(i)::value, BIG>(x, by, up); };
+      const std::integral_constant<int, 0> i0;
+      const std::integral_constant<int, 1> i1;
+      if constexpr (MODE == kMX4) {
+        const std::integral_constant<int, 2> i2;
+        const std::integral_constant<int, 3> i3;
+        step_mma(s, 2 * w, k(i0, a, f[0]), k(i0, b, f[1]), k(i1, a, f[0]), k(i1, b, f[1]));
+        step_mma(s, 2 * w + 1, k(i2, a, f[0]), k(i2, b, f[1]), k(i3, a, f[0]), k(i3, b, f[1]));
+      } else {
+        step_mma(s, w, k(i0, a, f[0]), k(i0, b, f[1]), k(i1, a, f[0]), k(i1, b, f[1]));
       }
     }
   }
@@ -491,26 +520,39 @@ struct Decode {
           out_mma(4 * w + e, mul_f16x2(x01[e], s01), mul_f16x2(y01[e], s01), mul_f16x2(x23[e], s23),
                   mul_f16x2(y23[e], s23), ph, pl);
       }
+    } else if constexpr (MODE == kMX4) {
+      const uint32_t most = max(max(vs[0], vs[1]), max(vs[2], vs[3]));
+      if (__any_sync(0xffffffffu, most > Mx<MODE>::largest(false))) mx_weigh<true>(vw, vs, ph, pl);
+      else mx_weigh<false>(vw, vs, ph, pl);
     } else {
-      const uint32_t f01 = mx_factor(vs[0]) | (mx_factor(vs[1]) << 16);
-      const uint32_t f23 = mx_factor(vs[2]) | (mx_factor(vs[3]) << 16);
-#pragma unroll
-      for (int w = 0; w < G::vw; ++w)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t sel = hf ? 0x7632u : 0x5410u;
-          const uint32_t u = __byte_perm(vw[0][w], vw[1][w], sel), v = __byte_perm(vw[2][w], vw[3][w], sel);
-          if constexpr (MODE == kMX4) {
-            out_mma(4 * w + 2 * hf, mx_pair<MODE, 0>(u, f01), mx_pair<MODE, 1>(u, f01),
-                    mx_pair<MODE, 0>(v, f23), mx_pair<MODE, 1>(v, f23), ph, pl);
-            out_mma(4 * w + 2 * hf + 1, mx_pair<MODE, 2>(u, f01), mx_pair<MODE, 3>(u, f01),
-                    mx_pair<MODE, 2>(v, f23), mx_pair<MODE, 3>(v, f23), ph, pl);
-          } else {
-            out_mma(2 * w + hf, mx_pair<MODE, 0>(u, f01), mx_pair<MODE, 1>(u, f01),
-                    mx_pair<MODE, 0>(v, f23), mx_pair<MODE, 1>(v, f23), ph, pl);
-          }
-        }
+      mx_weigh<true>(vw, vs, ph, pl);
     }
+  }
+
+  template <bool BIG>
+  __device__ __forceinline__ void mx_weigh(const uint32_t (&vw)[4][G::vw], const uint32_t (&vs)[4], const uint32_t (&ph)[NT][2],
+                                           const uint32_t (&pl)[NT][2]) {
+    constexpr uint32_t up = Mx<MODE>::up(false);
+    const uint32_t f01 = mx_factor<BIG>(vs[0], up) | (mx_factor<BIG>(vs[1], up) << 16);
+    const uint32_t f23 = mx_factor<BIG>(vs[2], up) | (mx_factor<BIG>(vs[3], up) << 16);
+#pragma unroll
+    for (int w = 0; w < G::vw; ++w)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t sel = hf ? 0x7632u : 0x5410u;
+        const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel), y = __byte_perm(vw[2][w], vw[3][w], sel);
+        auto v = [&](auto i, uint32_t c, uint32_t by) { return mx_pair<MODE, decltype(i)::value, BIG>(c, by, up); };
+        const std::integral_constant<int, 0> i0;
+        const std::integral_constant<int, 1> i1;
+        if constexpr (MODE == kMX4) {
+          const std::integral_constant<int, 2> i2;
+          const std::integral_constant<int, 3> i3;
+          out_mma(4 * w + 2 * hf, v(i0, x, f01), v(i1, x, f01), v(i0, y, f23), v(i1, y, f23), ph, pl);
+          out_mma(4 * w + 2 * hf + 1, v(i2, x, f01), v(i3, x, f01), v(i2, y, f23), v(i3, y, f23), ph, pl);
+        } else {
+          out_mma(2 * w + hf, v(i0, x, f01), v(i1, x, f01), v(i0, y, f23), v(i1, y, f23), ph, pl);
+        }
+      }
   }
 };
 

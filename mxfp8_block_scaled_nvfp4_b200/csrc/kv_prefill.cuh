@@ -125,19 +125,19 @@ template <int MODE>
 __host__ __device__ constexpr int octet(int p) {
   return MODE == kNV ? p : MODE == kMX4 ? (p & 1) * 4 + p / 2 : (p / 4) * 4 + (p & 1) * 2 + (p / 2 % 2);
 }
-// Eight codes (one word, MXFP8 two) times the scale pair f.
-template <int MODE>
-__device__ __forceinline__ uint4 decode8(const uint32_t* w, uint32_t f) {
+// Eight codes (one word, MXFP8 two) times the pair f of factors.
+template <int MODE, bool BIG>
+__device__ __forceinline__ uint4 decode8(const uint32_t* w, uint32_t f, uint32_t up) {
   if constexpr (MODE == kNV) {
     uint32_t v[4];
     e2m1x8_to_f16x2(w[0], v);
     return make_uint4(mul_f16x2(v[0], f), mul_f16x2(v[1], f), mul_f16x2(v[2], f), mul_f16x2(v[3], f));
   } else if constexpr (MODE == kMX4) {
-    return make_uint4(mx_pair<MODE, 0>(w[0], f), mx_pair<MODE, 1>(w[0], f),
-                      mx_pair<MODE, 2>(w[0], f), mx_pair<MODE, 3>(w[0], f));
+    return make_uint4(mx_pair<MODE, 0, BIG>(w[0], f, up), mx_pair<MODE, 1, BIG>(w[0], f, up),
+                      mx_pair<MODE, 2, BIG>(w[0], f, up), mx_pair<MODE, 3, BIG>(w[0], f, up));
   } else {
-    return make_uint4(mx_pair<MODE, 0>(w[0], f), mx_pair<MODE, 1>(w[0], f),
-                      mx_pair<MODE, 0>(w[1], f), mx_pair<MODE, 1>(w[1], f));
+    return make_uint4(mx_pair<MODE, 0, BIG>(w[0], f, up), mx_pair<MODE, 1, BIG>(w[0], f, up),
+                      mx_pair<MODE, 0, BIG>(w[1], f, up), mx_pair<MODE, 1, BIG>(w[1], f, up));
   }
 }
 
@@ -170,9 +170,10 @@ struct Raw {
     return first;
   }
   // Decodes the slots into row `tok` of a tile, elements e0 .. e0 + EPT, as
-  // 16-byte chunks: eight lanes (eight rows) cover eight chunk places.
+  // 16-byte chunks: eight lanes (eight rows) cover eight chunk places.  up: of
+  // the side (Mx).
   static __device__ __forceinline__ void decode(const AttnArgs& a, uint32_t at, uint32_t p, uint32_t first, bool there, uint32_t tile,
-                                                uint32_t tok, uint32_t e0) {
+                                                uint32_t tok, uint32_t e0, uint32_t up) {
     const uint32_t row = tile + (tok >> 3) * S::group + (tok & 7u) * 128u + (e0 >> 6) * 1024u, c0 = (e0 >> 3) & 7u;
     uint32_t s0, s1;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(at + S::raw_codes + 8u * p));
@@ -195,12 +196,19 @@ struct Raw {
         f[0] = __byte_perm(pr, 0, 0x1010);
         f[1] = __byte_perm(pr, 0, 0x3232);
       } else {
-        const uint32_t q = mx_factor((sc >> (8 * u)) & 255u);
-        f[0] = f[1] = q | (q << 16);
+        const uint32_t q = (sc >> (8 * u)) & 255u;
+        if (MODE == kMX8 || q > 254u - up) {
+          f[0] = mx_factor<true>(q, up) * 0x10001u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            st_shared_v4(row + (((c0 + (u * 4u + e)) ^ (tok & 7u)) << 4), decode8<MODE, true>(&w[e * wo], f[0], up));
+          continue;
+        }
+        f[0] = f[1] = mx_factor<false>(q, up) * 0x10001u;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        st_shared_v4(row + (((c0 + (u * 4u + e)) ^ (tok & 7u)) << 4), decode8<MODE>(&w[e * wo], f[e / 2]));
+        st_shared_v4(row + (((c0 + (u * 4u + e)) ^ (tok & 7u)) << 4), decode8<MODE, false>(&w[e * wo], f[e / 2], up));
     }
   }
 };
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     constexpr int up2 = kMx ? 16 : 14;
     const float up = pow2(up2 - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
     const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
-    fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(-up2), 1e-37f);
+    fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(Mx<MODE>::key_down - up2), 1e-37f);
     for (uint32_t o = half; o < a.D / 8u; o += 2u) {
       float x[8];
       load8<QT>(q + 8u * o, x);
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       }
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       W::decode(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile,
-                tok, e0);
+                tok, e0, Mx<MODE>::up(side == 0));
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0 && !(side == 1 && warp == 0 && withheld_stage(n))) arrive(smem_u32(&full[side][st]));
