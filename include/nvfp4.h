@@ -465,7 +465,9 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  * NVFP4_ERR_DEVICE_INDEX.
  * MX modes: a block scale above 2^64 (0xFF included) counts as 2^64, and
  * elements that are no multiples of 2^-133 (MXFP4 keys: of 2^-109) count as
- * the nearest one.
+ * the nearest one.  The NaN codes of MXFP8 (0x7F and 0xFF; inputs are finite,
+ * so none should be there) count as +-480: a NaN in a cache is not carried into
+ * the results, and kv_cache_read is where it shows.
  * Hq a multiple of heads, Hq <= 65535; B <= 65535; T*Hq*D at most 2^34;
  * B*heads*ceil(max_q*(Hq/heads)/8)*(max_kv/64 + 2) below 2^32.
  * workspace: device scratch, 16-byte aligned, contents undefined on entry

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import kv_reference
 from kv_reference import attention, cache_sides, check, seeded
 from test_gpu_kv_attention import compare, i32, make, nv  # noqa: F401 (nv is a fixture)
 
@@ -138,3 +139,33 @@ def test_mx_largest_values_over_a_long_range(nv, mode, n):
         # half a bf16 step, the weights' 2^-16 and the fp32 sums of 2^17 terms in four chains
         tol = 2.0 ** -9 + 2.0 ** -16 + (L / 4 + 160) * 2.0 ** -23
         assert ((out.double() / (most * 2.0 ** 64) - 1).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("n,D,page", [(1, 128, 16), (1, 96, 7), (1, 256, 64), (13, 64, 16), (40, 128, 16), (40, 96, 7), (70, 256, 64)])
+@pytest.mark.parametrize("L", [130, 2500])
+def test_nan_codes_count_as_480(nv, dtype, n, D, page, L, monkeypatch):
+    """kv_attention carries no NaN of an MXFP8 cache into its results: the codes
+    are +-480, for the queries that see their tokens and for no others;
+    kv_cache_read gives the NaN."""
+    heads, G, lens = 2, 3, [L, 120]
+    c, table = make(nv, "mxfp8", lens, heads, D, page, 93)
+    starts = [0, n, 2 * n]
+    q = seeded((2 * n, heads * G, D), 6, dtype)
+
+    def poison(side, b, j, head, element, code):
+        codes = (c.k_codes if side == "k" else c.v_codes).view(torch.uint8)
+        codes[int(table[b, j // page]), head, j % page, element] = code
+
+    poison("v", 0, L - 2 if n > 1 else L - 1, 0, 5, 0x7F)  # the last two tokens: few queries see them
+    poison("v", 0, L - n // 2 - 1, 0, 0, 0xFF)
+    poison("v", 0, 40, 1, D - 1, 0xFF)                     # all queries see it
+    poison("k", 1, 120 - n // 2 - 1, 1, 7, 0x7F)
+    at = int(table[0, 40 // page]) * page + 40 % page
+    assert torch.isnan(nv.kv_cache_read(c, i32([at]), dtype)[1][0, 1, D - 1])
+    table480 = kv_reference.E4M3.clone()
+    table480[0x7F], table480[0xFF] = 480.0, -480.0
+    monkeypatch.setattr(kv_reference, "E4M3", table480)
+    for window in (0, 60):
+        for kw in ({}, {"workspace": no_workspace()}):
+            compare(nv, c, table, lens, q, starts, n, L, window=window, **kw)
