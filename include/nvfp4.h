@@ -469,7 +469,7 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  * so none should be there) count as +-480: a NaN in a cache is not carried into
  * the results, and kv_cache_read is where it shows.
  * Hq a multiple of heads, Hq <= 65535; B <= 65535; T*Hq*D at most 2^34;
- * B*heads*ceil(max_q*(Hq/heads)/8)*(max_kv/64 + 2) below 2^32.
+ * B*heads*ceil(min(max_q, T)*(Hq/heads)/8)*(max_kv/64 + 2) below 2^32.
  * workspace: device scratch, 16-byte aligned, contents undefined on entry
  * and exit; with at least kv_attention_workspace_size bytes long sequences
  * are split over the SMs and joined, with less (NULL, 0 included) they are

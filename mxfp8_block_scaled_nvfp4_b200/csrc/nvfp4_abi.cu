@@ -949,6 +949,7 @@ constexpr int64_t kKvMaxWorkers = 148 * 4, kKvWorkers = 148;  // most, and fewes
 static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
                       int64_t window, bool prefill_has_it, size_t workspace_bytes) {
   KvPlan p;
+  if (max_q > T) max_q = T;
   const int64_t rows = max_q * (Hq / heads);
   // k_kv_decode decodes every code again for each 16 rows, k_kv_prefill once for
   // 256: NVFP4, 8 heads of 128, 8 sequences of 4096 tokens, 32 rows 39 us
@@ -1032,6 +1033,7 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
       (reinterpret_cast<uintptr_t>(page_table) & 3u))
     return fail(NVFP4_ERR_INVALID_ARG, "[%s] q, out and workspace must be 16-byte aligned (lse and the index arrays 4-byte)", tag);
   if (empty) return ok();
+  if (max_q > T) max_q = T;  // no sequence has more; the bound sizes the grids
   DeviceInfo d;
   st = device_info(tag, &d);
   if (st != NVFP4_OK) return st;

@@ -169,3 +169,16 @@ def test_nan_codes_count_as_480(nv, dtype, n, D, page, L, monkeypatch):
     for window in (0, 60):
         for kw in ({}, {"workspace": no_workspace()}):
             compare(nv, c, table, lens, q, starts, n, L, window=window, **kw)
+
+
+@pytest.mark.parametrize("heads,G,n", [(1, 8, 40), (2, 4, 3)])
+def test_a_loose_bound_on_the_queries(nv, heads, G, n):
+    """max_q may be any upper bound; no sequence has more than T queries."""
+    lens = [3000, 700]
+    c, table = make(nv, "nvfp4", lens, heads, 64, 16, 95)
+    q = seeded((2 * n, heads * G, 64), 7, bf16)
+    for starts in ([0, n, 2 * n], [0, 2 * n - 1, 2 * n]):
+        want = compare(nv, c, table, lens, q, starts, 2 * n, 3000)
+        for loose in (2 * n + 1, 1 << 20, 1 << 30):
+            got = compare(nv, c, table, lens, q, starts, loose, 3000)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
