@@ -543,7 +543,9 @@ class KvCache:
     and the sizes they hold.  codes int32 [num_pages, heads, page_size, D/8]
     (D/4 for "mxfp8"), scales uint8 [num_pages, heads, page_size, D/16]
     ("nvfp4") or D/32; g_k, g_v fp32 [1] or None ("nvfp4" only, both or
-    neither).  The handle keeps references to the tensors and no copy."""
+    neither).  The handle keeps references to the tensors and no copy, and
+    their addresses with them: its attributes cannot be set (a cache in other
+    tensors is another handle), and the tensors' storage must stay in place."""
 
     def __init__(self, mode: str, k_codes, k_scales, v_codes, v_scales, g_k=None, g_v=None):
         if mode not in MODE:
@@ -563,13 +565,17 @@ class KvCache:
         _need_g(g_k, 1, "g_k")
         _need_g(g_v, 1, "g_v")
         _need_cuda(k_codes, k_scales, v_codes, v_scales, g_k, g_v)
-        self.mode, self.num_pages, self.heads, self.page_size, self.D = mode, P, H, R, D
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.g_k, self.g_v = g_k, g_v
-        self.device = k_codes.device
-        self._args = KvCacheArgs(MODE[mode], P, R, H, D, *(None if t is None else t.data_ptr() for t in (
+        args = KvCacheArgs(MODE[mode], P, R, H, D, *(None if t is None else t.data_ptr() for t in (
             k_codes, k_scales, v_codes, v_scales, g_k, g_v)))
-        self._ref = ctypes.byref(self._args)
+        self.__dict__.update(mode=mode, num_pages=P, heads=H, page_size=R, D=D, k_codes=k_codes, k_scales=k_scales,
+                             v_codes=v_codes, v_scales=v_scales, g_k=g_k, g_v=g_v, device=k_codes.device, _args=args,
+                             _ref=ctypes.byref(args))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KvCache.{name} cannot be set: the handle holds its tensors' addresses; make a new one")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"KvCache.{name} cannot be deleted")
 
     @classmethod
     def empty(cls, mode: str, num_pages: int, heads: int, page_size: int, D: int, g_k=None, g_v=None, device="cuda"):

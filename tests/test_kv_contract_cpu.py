@@ -14,3 +14,27 @@ def test_max_q_beyond_all_queries_is_all_queries(L):
             # the grids' limits
             assert needs_device(attend(L, cache(heads=64), q_start=A, T=T, Hq=256, stride=256 * 64, max_q=loose)), msg(L)
             assert needs_device(attend(L, cache(mode=1), dt=1, q_start=A, T=T, max_q=loose, max_kv=1024, max_pages=64)), msg(L)
+
+
+def host_cache(monkeypatch, mode="nvfp4"):
+    """A handle over host tensors (no call is made with it)."""
+    monkeypatch.setattr(nv, "_need_cuda", lambda *ts: None)
+    g = [torch.ones(1), torch.ones(1)] if mode == "nvfp4" else [None, None]
+    return nv.KvCache.empty(mode, 4, 2, 16, 64, *g, device="cpu")
+
+
+@pytest.mark.parametrize("mode", ["nvfp4", "mxfp8"])
+def test_a_cache_handle_cannot_be_given_other_tensors(monkeypatch, mode):
+    """The library reads the addresses the handle was made with."""
+    c = host_cache(monkeypatch, mode)
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales", "g_k", "g_v", "mode", "num_pages", "page_size", "heads", "D",
+                 "device", "_args", "_ref", "anything"):
+        before = getattr(c, name, None)
+        with pytest.raises(AttributeError, match="cannot be set"):
+            setattr(c, name, torch.ones(1))
+        assert getattr(c, name, None) is before
+    with pytest.raises(AttributeError):
+        del c.k_codes
+    assert c._args.k_codes == c.k_codes.data_ptr() and c._args.v_scales == c.v_scales.data_ptr()
+    assert c._args.g_k == (c.g_k.data_ptr() if mode == "nvfp4" else None)
+    assert (c._args.D, c._args.heads, c._args.page_size, c._args.num_pages) == (64, 2, 16, 4)
