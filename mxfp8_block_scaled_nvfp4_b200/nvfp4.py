@@ -116,10 +116,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The raw handle of a device's current stream; building a torch.cuda.Stream
+# object takes longer than a small launch.  (Not a public name of torch.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream():
-    """The current stream of the current device as a pointer (the raw handle:
-    building a torch.cuda.Stream object takes longer than a small launch)."""
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    """The current stream of the current device as a pointer."""
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def _need_cuda(*ts):

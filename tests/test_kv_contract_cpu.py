@@ -1,4 +1,7 @@
 """Host-side contract of the key/value cache calls that no GPU is needed for."""
+import importlib.util
+import types
+
 import pytest
 import torch
 
@@ -38,3 +41,19 @@ def test_a_cache_handle_cannot_be_given_other_tensors(monkeypatch, mode):
     assert c._args.k_codes == c.k_codes.data_ptr() and c._args.v_scales == c.v_scales.data_ptr()
     assert c._args.g_k == (c.g_k.data_ptr() if mode == "nvfp4" else None)
     assert (c._args.D, c._args.heads, c._args.page_size, c._args.num_pages) == (64, 2, 16, 4)
+
+
+def test_the_stream_without_torchs_private_accessor(monkeypatch):
+    """_stream() serves every call of the binding and must not depend on a name
+    that torch does not promise."""
+    spec = importlib.util.find_spec(nv.__name__)
+    for private in (True, False):
+        if private:
+            monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+        else:
+            monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+            monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=2000 + device))
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+        assert m._stream().value == (1003 if private else 2003)
