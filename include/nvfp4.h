@@ -396,8 +396,10 @@ NVFP4_API nvfp4_status gather_qmm_noalloc(const void* x, const uint32_t* w_codes
  * fixed for the cache's life: blocks beyond them saturate.
  * D % 32 == 0 and 32 <= D <= 256 (beyond: NVFP4_ERR_UNSUPPORTED);
  * heads <= 65535; page_size >= 1; num_pages * page_size < 2^31 (byte offsets
- * are 64-bit).  Rows that were never written may hold any bytes: no call
- * reads a row its arguments do not name.
+ * are 64-bit).  Rows that were never written may hold any bytes: a row that a
+ * call's arguments do not name has no effect on its results (kv_attention may
+ * read some all the same, never outside the four arrays), so another stream may
+ * write such rows meanwhile.
  * The struct is read on the host during the call. */
 typedef struct {
   nvfp4_mode mode;
@@ -418,8 +420,9 @@ typedef struct {
  * mxfp8_quantize or mxfp4_quantize would give it (LINEAR).  Other rows are
  * left as they are.
  * k, v [T, heads, D] of dt (fp32, fp16, bf16): heads and D contiguous, tokens
- * k_stride and v_stride elements apart (>= heads*D, or any value for T <= 1;
- * a multiple of 16 bytes), so both may be parts of one projection's rows.
+ * k_stride and v_stride elements apart (>= heads*D and below 2^31, or any value
+ * for T <= 1; a multiple of 16 bytes), so both may be parts of one projection's
+ * rows.
  * slots [T] int32: a negative slot skips its token; a slot past the cache
  * skips it and sets NVFP4_ERR_DEVICE_INDEX.  The slots of one call must
  * differ (which token's bytes a repeated slot ends with is unspecified).
@@ -450,7 +453,8 @@ NVFP4_API nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t*
  * out and lse NaN, and no others.  Query head h reads key/value
  * head h / (Hq / heads).
  * q: fp16 or bf16, [T, Hq, D], heads and D contiguous, tokens q_stride
- * elements apart (>= Hq*D, or any value for T <= 1; a multiple of 16 bytes).
+ * elements apart (>= Hq*D and below 2^31, or any value for T <= 1; a multiple of
+ * 16 bytes).
  * q_start [B+1] int32: the queries of sequence b are tokens q_start[b] ..
  * q_start[b+1]-1 (0 <= q_start[b] <= q_start[b+1] <= T, at most max_q of
  * them); NULL: one query a sequence, token b (T == B, max_q == 1).

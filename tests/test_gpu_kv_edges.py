@@ -182,3 +182,24 @@ def test_a_loose_bound_on_the_queries(nv, heads, G, n):
         for loose in (2 * n + 1, 1 << 20, 1 << 30):
             got = compare(nv, c, table, lens, q, starts, loose, 3000)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("n,D,page", [(1, 128, 16), (1, 96, 24), (1, 64, 7), (40, 128, 64), (40, 96, 24), (40, 256, 7)])
+def test_rows_without_a_name_have_no_effect(nv, mode, n, D, page):
+    lens, heads = [150, 37], 2
+    c, table = make(nv, mode, lens, heads, D, page, 97)
+    q = seeded((2 * n, heads * 4, D), 8, bf16)
+    named = torch.zeros(c.num_pages, page, dtype=torch.bool)
+    for b, length in enumerate(lens):
+        j = torch.arange(length)
+        named[table[b].cpu().long()[j // page], j % page] = True
+    other = ~named[:, None, :, None].cuda()
+    results = []
+    for byte in (0xFF, 0x7F, 0x00, 0x5A):
+        for t in (c.k_codes, c.v_codes, c.k_scales, c.v_scales):
+            t.copy_(torch.where(other, torch.full_like(t.view(torch.uint8), byte).view(t.dtype), t))
+        results.append(nv.kv_attention(c, q, table, i32(lens), i32([0, n, 2 * n]), n, 150, return_lse=True))
+        nv.check_device_errors()
+    assert torch.isfinite(results[0][0].float()).all()
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))

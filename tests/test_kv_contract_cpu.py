@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from mxfp8_block_scaled_nvfp4_b200 import nvfp4 as nv
-from test_kv_cpu import A, L, attend, cache, msg, needs_device  # noqa: F401 (L is a fixture)
+from test_kv_cpu import A, L, attend, cache, msg, needs_device, write  # noqa: F401 (L is a fixture)
 
 
 def test_max_q_beyond_all_queries_is_all_queries(L):
@@ -17,6 +17,13 @@ def test_max_q_beyond_all_queries_is_all_queries(L):
             # the grids' limits
             assert needs_device(attend(L, cache(heads=64), q_start=A, T=T, Hq=256, stride=256 * 64, max_q=loose)), msg(L)
             assert needs_device(attend(L, cache(mode=1), dt=1, q_start=A, T=T, max_q=loose, max_kv=1024, max_pages=64)), msg(L)
+
+
+def test_token_strides_end_at_2_to_the_31(L):
+    c = cache()
+    for big, ok in ((2 ** 31 - 8, True), (2 ** 31, False), (2 ** 62, False)):
+        assert needs_device(write(L, c, ks=big, vs=big)) == ok and needs_device(attend(L, c, stride=big)) == ok
+        assert needs_device(write(L, c, T=1, ks=big, vs=big)) and needs_device(attend(L, c, q_start=A, B=1, T=1, stride=big))
 
 
 def host_cache(monkeypatch, mode="nvfp4"):
