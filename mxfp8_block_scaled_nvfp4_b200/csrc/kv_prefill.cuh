@@ -66,6 +66,9 @@ struct Shape {
   static constexpr uint32_t tm_s = 0, tm_o = 256;     // TMEM columns: S of tile t at 128 t, O at 256 + 128 t
 };
 
+// Through L1, unlike copy16: a thread's 16-byte pieces are parts of lines that
+// its neighbours read too (2048 over 4096 tokens MXFP8 217 us, past L1 228;
+// MXFP4 181 and 184; 4096 over 8192 NVFP4 528 and 526).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -75,16 +78,6 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t at) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at));
   return v;
 }
 __device__ __forceinline__ void st_shared_u8(uint32_t at, uint32_t v) {
