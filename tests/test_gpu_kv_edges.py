@@ -203,3 +203,63 @@ def test_rows_without_a_name_have_no_effect(nv, mode, n, D, page):
         nv.check_device_errors()
     assert torch.isfinite(results[0][0].float()).all()
     assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("page", [16, 24])
+def test_tokens_on_bad_pages_count_as_unseen(nv, mode, dtype, n, page):
+    lens, heads, G, D = [170, 90], 2, 4, 64
+    c, table = make(nv, mode, lens, heads, D, page, 61)
+    q = seeded((2 * n, heads * G, D), 1, dtype)
+    starts = [0, n, 2 * n]
+    sides = cache_sides(c)
+    for bad in ([0], [2, 4], list(range(-(-170 // page)))):
+        for entry in (c.num_pages, -1, 2 ** 31 - 1):
+            t = table.clone()
+            t[0, bad] = entry
+            out, lse = nv.kv_attention(c, q, t, i32(lens), i32(starts), n, 170, return_lse=True)
+            with pytest.raises(nv.Nvfp4Error) as e:
+                nv.check_device_errors()
+            assert e.value.status == nv.ERR_DEVICE_INDEX
+            # the reference without those tokens: softmax over the rest
+            o, l, tol, ltol = seen_without(sides, q, table, lens, starts, D ** -0.5, {0: bad})
+            check(out, o, tol, "out")
+            check(lse, l, ltol, "lse")
+
+
+def seen_without(sides, q, table, lens, starts, scale, bad):
+    """attention() with the tokens of pages bad[b] of sequence b left out: a
+    query at position p over the tokens that are left is the last query over the
+    cache that holds only those."""
+    page = sides[0].shape[2]
+    rows = [attention(sides, q, table, torch.tensor(lens), torch.tensor(starts), scale)]
+    out, lse, tol, ltol = rows[0]
+    for b, pages in bad.items():
+        for i in range(starts[b + 1] - starts[b]):
+            t, p = starts[b] + i, lens[b] - (starts[b + 1] - starts[b]) + i
+            kept = [j for j in range(max(0, p + 1)) if j // page not in pages]
+            at = table[b].cpu().long()
+            j = torch.tensor(kept, dtype=torch.long)
+            K, V = (s[at[j // page], :, j % page].transpose(0, 1)[None] for s in sides)  # one page [1, H, kept, D]
+            r = attention((K, V), q[t:t + 1], torch.zeros(1, 1), torch.tensor([len(kept)]), None, scale)
+            out[t], lse[t], tol[t], ltol[t] = (x[0] for x in r)
+    return out, lse, tol, ltol
+
+
+@pytest.mark.parametrize("mode,dtype", [("nvfp4", bf16), ("mxfp4", f16), ("mxfp8", bf16)])
+@pytest.mark.parametrize("lens,n", [([5000, 700], [1, 1]), ([4097], [3]), ([2047, 4100], [130, 40])])
+def test_a_workspace_of_the_stated_size_is_enough(nv, mode, dtype, lens, n):
+    starts = [0]
+    for x in n:
+        starts.append(starts[-1] + x)
+    c, table = make(nv, mode, lens, 2, 128, 64, 31)
+    q = seeded((starts[-1], 8, 128), 7, dtype)
+    size = nv.kv_attention_workspace_size(len(lens), starts[-1], 8, 2, 128, max(n), max(lens), 0)
+    assert size > 0
+    for part in (size, size // 2 // 16 * 16, size // 5 // 16 * 16):
+        guard = 1 << 20
+        both = torch.full((part + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+        compare(nv, c, table, lens, q, starts, max(n), max(lens), workspace=both[:part])
+        assert (both[part:] == 0xA5).all()

@@ -19,6 +19,31 @@ def test_max_q_beyond_all_queries_is_all_queries(L):
             assert needs_device(attend(L, cache(mode=1), dt=1, q_start=A, T=T, max_q=loose, max_kv=1024, max_pages=64)), msg(L)
 
 
+def decode_bytes(rows, D):
+    """k_kv_decode: 592 workers, two partial results of a row tile and 32 bytes each."""
+    tile = 8 if rows <= 8 or D > 128 else 16
+    return 592 * (2 * tile * (4 * D + 8) + 32)
+
+
+@pytest.mark.parametrize("args,want", [
+    # B, T, Hq, heads, D, max_q, max_kv, window
+    ((1, 1, 32, 8, 128, 1, 64), 0),                                    # one unit of tokens: nothing to split
+    ((1, 1, 32, 8, 128, 1, 65), decode_bytes(4, 128)),
+    ((32, 32, 32, 8, 128, 1, 32768), decode_bytes(4, 128)),            # the same for any batch and length
+    ((8, 8, 16, 8, 256, 1, 6000), decode_bytes(2, 256)),
+    ((2, 6, 32, 8, 128, 3, 5000), decode_bytes(12, 128)),
+    # one sequence of 100 queries, group 4: 8 heads x 2 tiles of 256 rows, 8192 * 16 / 148 = 885.6 tokens a CTA, so
+    # chunks of 896: 10 of them
+    ((1, 100, 32, 8, 128, 100, 8192), 10 * 100 * 32 * (4 * 128 + 8)),
+    # 8 x 300 over 2500 and the like: 320 tiles, more than there are SMs, so not split
+    ((8, 2400, 32, 8, 128, 300, 2500), decode_bytes(1200, 128)),
+    # a window of 1024 leaves 1024 + 100 + 30 tokens, at least 512 a chunk
+    ((1, 100, 32, 8, 128, 100, 8192, 1024), max(3 * 100 * 32 * (4 * 128 + 8), decode_bytes(400, 128))),
+])
+def test_workspace_sizes(L, args, want):
+    assert nv.kv_attention_workspace_size(*args) == want
+
+
 def test_token_strides_end_at_2_to_the_31(L):
     c = cache()
     for big, ok in ((2 ** 31 - 8, True), (2 ** 31, False), (2 ** 62, False)):
