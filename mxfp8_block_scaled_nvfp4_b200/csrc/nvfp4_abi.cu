@@ -951,11 +951,17 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   KvPlan p;
   if (max_q > T) max_q = T;
   const int64_t rows = max_q * (Hq / heads);
-  // k_kv_decode decodes every code again for each 16 rows, k_kv_prefill once for
-  // 256: NVFP4, 8 heads of 128, 8 sequences of 4096 tokens, 32 rows 39 us
-  // against 49, 48 rows 49 against 51, 64 rows 60 against 53 (one sequence of
-  // 32768: 43 / 50, 58 / 51, 73 / 51)
-  p.prefill = prefill_has_it && rows > 32;
+  // k_kv_decode decodes every code again for each 16 rows (8 above D 128),
+  // k_kv_prefill once for 256 (128).  8 heads, group 4, us (k_kv_decode /
+  // k_kv_prefill) of 8 sequences of 4096 tokens, and of one of 32768:
+  //   D 64, 48 rows   NVFP4 31 / 41, 37 / 39   MXFP4 37 / 46, 45 / 45
+  //         64 rows         36 / 42, 44 / 40         45 / 47, 55 / 45
+  //   D 128, 32 rows        38 / 50, 43 / 50         52 / 56, 61 / 57
+  //          48 rows        49 / 51, 58 / 50         70 / 58, 83 / 57
+  //   D 256, 16 rows        54 / 69, 63 / 69         76 / 79, 92 / 79
+  //          24 rows        71 / 70, 89 / 70        103 / 80, 131 / 80
+  // MXFP8 as MXFP4 (60 / 60, 69 / 60 at D 128 and 32 rows).
+  p.prefill = prefill_has_it && rows > (D <= 64 ? 48 : D <= 128 ? 32 : 16);
   p.chunk = p.chunks = 1;
   if (!p.prefill) {
     p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;  // D 256: two n-tiles would take more registers than there are

@@ -263,3 +263,15 @@ def test_a_workspace_of_the_stated_size_is_enough(nv, mode, dtype, lens, n):
         both = torch.full((part + guard,), 0xA5, dtype=torch.uint8, device="cuda")
         compare(nv, c, table, lens, q, starts, max(n), max(lens), workspace=both[:part])
         assert (both[part:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("mode,dtype", [("nvfp4", bf16), ("nvfp4", f16), ("mxfp4", bf16), ("mxfp8", bf16)])
+@pytest.mark.parametrize("D,border", [(32, 48), (64, 48), (96, 32), (128, 32), (160, 16), (256, 16)])
+def test_both_sides_of_the_border_between_the_kernels(nv, mode, dtype, D, border):
+    """The most rows a key/value head that k_kv_decode takes, and one query more."""
+    lens = [700, 90]
+    c, table = make(nv, mode, lens, 2, D, 16, 99)
+    for n in (border // 4, border // 4 + 1):
+        q = seeded((2 * n, 8, D), 9, dtype)
+        compare(nv, c, table, lens, q, [0, n, 2 * n], n, 700)
+        compare(nv, c, table, lens, q, [0, 2 * n - 1, 2 * n], 2 * n - 1, 700, window=50)
