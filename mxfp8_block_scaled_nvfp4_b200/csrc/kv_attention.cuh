@@ -131,11 +131,14 @@ __device__ __forceinline__ float ex2(float x) {
 //   O^T [16 elements x 8 rows] += V_hat^T . P^T
 // P^T is S^T's fragment transposed by movmatrix.
 //
-// Measured (NVFP4, 32 query and 8 key/value heads of 128): 32 x 32768 tokens
-// 196 us, 4.66 TB/s or 71 % of the copy rate; 1 x 131072 46 us, of which 5 are
-// spent up to the first unit (lengths, page table, codes: three loads one
-// after the other) and 3 in the join.  Bound by memory and by the decoding
-// instructions (660 for 32 tokens, the ALU pipe half busy) alike.
+// Measured (NVFP4, 32 query and 8 key/value heads of 128), in a captured graph:
+// 32 x 32768 tokens 196 us, 4.67 TB/s or 71 % of the copy rate; 1 x 131072
+// 46 us, of which 5 are spent up to the first unit (lengths, page table, codes:
+// three loads one after the other) and 3 in the join.  Calls on a stream take 2
+// to 4 us more each (the gap between launches), and seconds of the first case on
+// end 214 us: the 1000 W power cap takes the SM clock from 1965 to 1820 MHz.
+// Bound by memory and by the decoding instructions (660 for 32 tokens, the ALU
+// pipe half busy) alike.
 //
 // Number formats.  NVFP4: code * block scale has six significant bits and
 // lies in [2^-10, 2688], so K_hat and V_hat are exact in fp16 (the global
@@ -162,8 +165,10 @@ struct Geo {
   static constexpr int vbytes = DP / 8 * (int)Fmt<MODE>::bits / 8, vw = vbytes / 4;  // and of a value row
   static constexpr int ksteps = DP / 16, mtiles = DP / 16;
   static constexpr int krow = DP * (int)Fmt<MODE>::bits / 8, srow = DP / (int)Fmt<MODE>::group;  // a row's bytes
-  // 16-token tiles of a warp in a unit, units in shared memory: about 64 KB a
-  // CTA, three CTAs an SM
+  // 16-token tiles of a warp in a unit, units in shared memory: 34 to 66 KB of
+  // them a CTA.  With the fp32 output tiles of the four warps that is 45 to 73 KB
+  // (three CTAs an SM) for 8 rows of D <= 128, 53 to 100 KB (two, or one where
+  // the registers end first) for 16 rows and for D 256.
   static constexpr int ts = DP == 256 || (MODE == kMX8 && DP == 128) ? 1 : 2;
   static constexpr int unit = 16 * kDecWarps * ts, unit_bytes = 2 * unit * (krow + srow);
   static constexpr int stages = unit_bytes > 26000 ? 2 : unit_bytes > 12000 ? 3 : 4;

@@ -25,16 +25,18 @@
 // transpose.
 //
 // Measured: 4096 queries over 8192 tokens (NVFP4, 32 / 8 heads of 128, causal)
-// 527 us, 782 TFLOP/s or 48 % of the bf16 burst rate, with the SM clock near
-// 1.5 GHz under the power cap.  A tile of 128 tokens takes about 4500 clocks
-// for 2048 of products: the chain from S over the exponentials (3000) to P V
-// and the next S bounds it.  Tiles of 64 tokens with two S buffers hid more of
-// the chain, but an N = 64 product takes as long as an N = 128 one (671 us).
+// 528 us, 780 TFLOP/s or 48 % of the bf16 burst rate, at an SM clock of 1.83 GHz
+// (by the SMs' own counter; 970 W).  With 148 CTAs of two query tiles, a tile of
+// 128 tokens takes 2.78 us, about 5000 clocks for 2048 of products (MXFP4 3.38,
+// MXFP8 3.95, which have half as many products again), and a CTA 15 us besides:
+// the chain from S over the exponentials to P V and the next S bounds it.  Tiles
+// of 64 tokens with two S buffers hid more of the chain, but an N = 64 product
+// takes as long as an N = 128 one (671 us).
 //
-// Number formats as in k_kv_decode: NVFP4 exact fp16 operands, P times 2^7 in fp16; MX
-// modes exact bf16 operands and P in two bf16 terms, each with
-// its own MMA.  (fp16 queries over an MX cache would need two terms of Q as
-// well; they stay with k_kv_decode.)
+// Number formats as in k_kv_decode: NVFP4 exact fp16 operands, P times 2^7 in
+// fp16; MX modes exact bf16 operands and P in two bf16 terms, each with its own
+// MMA.  (fp16 queries over an MX cache would need two terms of Q as well; they
+// stay with k_kv_decode.)
 #pragma once
 
 #include "kv_attention.cuh"
