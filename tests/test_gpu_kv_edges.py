@@ -119,6 +119,34 @@ def test_mx_blocks_far_from_one(nv, mode, dtype, n, kexp, vexp):
 
 
 @pytest.mark.parametrize("mode", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_mx_scale_bytes_from_the_smallest_on(nv, mode, dtype, n, D):
+    """Value blocks with the scale bytes 0, 1, 2, ... in the outputs' elements
+    beside one another, and around the border of one factor (2 for MXFP4, whose
+    keys have theirs at 2^25)."""
+    L = 150
+    c, table = make(nv, mode, [L], 1, D, 16, 48)
+    q = seeded((n, 4, D), 4, dtype)
+    blocks = D // 32
+    for first in (0, 60, 126, 187):
+        c.v_scales.copy_((first + torch.arange(blocks, device="cuda") % 5).to(torch.uint8).expand_as(c.v_scales))
+        sides = cache_sides(c)
+        out = nv.kv_attention(c, q, table, i32([L]), i32([0, n]), n, L)
+        nv.check_device_errors()
+        o, _, tol, _ = attention(sides, q, table, torch.tensor([L]), torch.tensor([0, n]), D ** -0.5)
+        if dtype == f16:  # beyond fp16
+            o[o.abs() > 60000] = float("nan")
+        check(out, o, tol, "out")
+    for byte in (90, 152, 153):
+        c.v_scales.fill_(127)
+        c.k_scales.fill_(byte)
+        scale = D ** -0.5 * 2.0 ** (127 - byte) / 8
+        compare(nv, c, table, [L], q, [0, n], n, L, scale=scale)
+
+
+@pytest.mark.parametrize("mode", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("n", [1, 40])
 def test_mx_largest_values_over_a_long_range(nv, mode, n):
     """Values of 2^64 times the largest code, equal weights after a rise of the
