@@ -116,7 +116,8 @@ __device__ __forceinline__ float ex2(float x) {
 // uneven lengths, few heads and one long sequence fill the SMs alike (with a
 // grid of equal chunks the last wave stood half empty: one sequence of
 // 131072 tokens took 55 us in 2.4 waves, 47 us in one).  A run begins and
-// ends anywhere in a range: what it does not cover whole goes to k_kv_join.
+// ends anywhere in a range: what it does not cover whole goes to
+// k_kv_decode_join.
 //
 // In a CTA a fifth warp copies the units ahead into shared memory, so loads
 // cost the other four neither instructions nor registers: one bulk copy a page
@@ -229,8 +230,9 @@ __device__ __forceinline__ uint32_t e2m1_pair_bf16(uint32_t w) {
 // Bytes i and i + 2 of a word as bf16 pairs holding 2^-120 times the e4m3 value.
 // The NaN codes (0x7F, 0xFF) read as +-480: finite, so that a weight of zero
 // hides them from the queries that do not see their token.  Carrying a NaN to
-// those that do costs a check of every code (16 x 8192, D 128, 59.8 us for 58.0;
-// 8 x 6000, D 256, 59.6 for 55.5), for inputs that the library leaves open.
+// those that do costs a check of every code (in the best ways tried 16 x 8192 of
+// D 128 took 59.8 us for 58.0, 8 x 6000 of D 256 59.6 for 55.5), for inputs that
+// the library leaves open.
 template <int I>
 __device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w) {
   const uint32_t sg = I == 0 ? w << 8 : w;
@@ -253,7 +255,7 @@ struct Mx {
   __device__ static constexpr uint32_t up(bool key) { return left_out - (key ? key_down : 0); }
   __device__ static constexpr uint32_t largest(bool key) { return 254u - up(key); }  // scale byte that one factor holds
 };
-// The factor of a block, to be multiplied with pairs after `first`.
+// A block's factor; in a BIG tile what the pair functions leave out is another.
 template <bool BIG>
 __device__ __forceinline__ uint32_t mx_factor(uint32_t s, uint32_t up) {
   return BIG ? max(min(s, 191u) << 7, 0x40u) : (s + up) << 7;
