@@ -265,7 +265,8 @@ def prepare(case, seed):
         fill(st, case, seed)
         perm = torch.randperm(2 * rows, generator=order) if each < 64 else torch.arange(2 * rows)
         st.update(case=case, src=perm[:rows].to(torch.int32).cuda(), dst=perm[rows:].to(torch.int32).cuda(),
-                  starts=(torch.arange(S + 1) * each).to(torch.int32).cuda())
+                  # a few drafts of each sequence, one after the other; of a copied prefix every row for itself
+                  starts=(torch.arange(S + 1) * each).to(torch.int32).cuda() if each < 64 else None)
         return st
     kv, n = lengths(case)
     need = [-(-m // P) for m in kv]
