@@ -395,8 +395,10 @@ def run_own(st):
             y, h, r = nv.rms_norm(st["x"], st["w"], EPS, st["residual"], return_rstd=True)
         else:
             codes, scales, h, r = nv.rms_norm_quantize(st["x"], st["w"], c["mode"], st["g"], EPS, st["residual"], "swizzled", return_rstd=True)
-            back = {"nvfp4": nv.nvfp4_dequantize, "mxfp8": nv.mxfp8_dequantize, "mxfp4": nv.mxfp4_dequantize}[c["mode"]]
-            y = back(codes, scales, c["K"], st["g"], "swizzled", dtype) if c["mode"] == "nvfp4" else back(codes, scales, c["K"], "swizzled", dtype)
+            if c["mode"] == "nvfp4":
+                y = nv.nvfp4_dequantize(codes, scales, st["g"], "swizzled", dtype)
+            else:
+                y = (nv.mxfp8_dequantize if c["mode"] == "mxfp8" else nv.mxfp4_dequantize)(codes, scales, "swizzled", dtype)
         return (y, r) if st["residual"] is None else (y, r, h)
     if c["op"] == "norm_grad":
         return nv.rms_norm_vjp(st["dy"], st["h"], st["w"], st["rstd"], st["dh"])
