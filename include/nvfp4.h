@@ -381,6 +381,53 @@ NVFP4_API nvfp4_status gather_qmm_noalloc(const void* x, const uint32_t* w_codes
                                           int64_t E, int64_t N, int64_t K, void* y, nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Root-mean-square norm in front of a block-scaled product.  (No page
+ * counterpart.)
+ *
+ * Per row of K elements, dt the type of x, residual, w, h and y:
+ *   h = dt(x + residual)  (h = x where residual is NULL),
+ *   r = fp32(1 / sqrt(sum_k h_k^2 / K + eps)), sum and root in fp64,
+ *   y_k = fp32(fp32(h_k * r) * w_k).
+ * K a multiple of 16 (32 for the MX modes) and at most 32768 (beyond:
+ * NVFP4_ERR_UNSUPPORTED); rows*K at most 2^34; eps in [2^-126, 2^126].
+ * x, residual [rows, K]; w [K]; h [rows, K], written: given with a residual
+ * and only then, it may be x or residual itself.  rstd [rows] fp32 or NULL
+ * gets r (rms_norm_vjp takes it). */
+
+/* rms_norm -- y [rows, K] of dt, rounded once (for products that quantize
+ * their input themselves: qmv, gather_qmm). */
+NVFP4_API nvfp4_status rms_norm(const void* x, const void* residual, const void* w, nvfp4_dtype dt, int64_t rows,
+                                int64_t K, double eps, void* h, void* y, float* rstd, nvfp4_stream_t stream);
+
+/* rms_norm_quantize -- y as codes and scales: exactly what nvfp4_quantize,
+ * mxfp8_quantize or mxfp4_quantize would give for the fp32 matrix y (codes
+ * [rows, K/8], MXFP8 K/4; scales in `layout`, padding included; g, NVFP4 only,
+ * the calibrated amax of y: blocks beyond it saturate). */
+NVFP4_API nvfp4_status rms_norm_quantize(nvfp4_mode mode, const void* x, const void* residual, const void* w,
+                                         nvfp4_dtype dt, int64_t rows, int64_t K, double eps, const float* g, void* h,
+                                         uint32_t* codes, uint8_t* scales, nvfp4_layout layout, float* rstd,
+                                         nvfp4_stream_t stream);
+
+/* rms_norm_vjp -- gradients of both (a quantized y passes its gradient
+ * straight through, as in the backward pass of qqmm).  With dy the gradient of
+ * y and dh the gradient that reaches h past the norm (NULL: none):
+ *   dx = dt(dh + r (w dy - h r^2 s / K)),  s = sum_k w_k dy_k h_k,
+ *   dw_k = sum over the rows of dy_k h_k r   (fp32, the same bits every time).
+ * dx, the gradient of x and of residual alike, [rows, K]; it may be dy or dh
+ * itself.  dw [K] fp32, overwritten, or NULL.  dy, h, dh [rows, K] and w [K]
+ * of dt; rstd [rows] as rms_norm gave it.
+ * workspace: device scratch of rms_norm_vjp_workspace_size(rows, K) bytes,
+ * 16-byte aligned, contents undefined on entry and exit; needed for dw alone.
+ * Calls that may overlap need one each. */
+NVFP4_API nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                                    nvfp4_dtype dt, int64_t rows, int64_t K, void* dx, float* dw, void* workspace,
+                                    size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Bytes of workspace that rms_norm_vjp needs for dw; 0 for sizes it rejects
+ * and for no rows.  Host only. */
+NVFP4_API size_t rms_norm_vjp_workspace_size(int64_t rows, int64_t K);
+
+/* ---------------------------------------------------------------------------
  * Paged key/value cache held in NVFP4, MXFP8 or MXFP4, and attention over it.
  * (No page counterpart: the formats and the per-block arithmetic are those
  * of the quantizers above; the cache layout is this library's.)
@@ -430,6 +477,42 @@ typedef struct {
 NVFP4_API nvfp4_status kv_cache_write(const nvfp4_kv_cache* cache, const void* k, const void* v, nvfp4_dtype dt,
                                       int64_t T, int64_t k_stride, int64_t v_stride, const int32_t* slots,
                                       nvfp4_stream_t stream);
+
+/* kv_cache_append -- kv_cache_write with the rotation of queries and keys by
+ * their positions on the way (one launch).  Of every head of q and k the first
+ * `rot` elements (a multiple of 16, at most D) turn by the angles of the
+ * token's position p: with c = cos[p, i], s = sin[p, i], i < rot/2,
+ *   (a, b) -> (fp32(fp32(a c) - fp32(b s)), fp32(fp32(b c) + fp32(a s))),
+ * (a, b) = elements (i, i + rot/2), or (2i, 2i + 1) when interleaved.
+ * Keys are quantized as these fp32 numbers, queries rounded to dt; values are
+ * written as kv_cache_write does.
+ * q [T, Hq, D], k, v [T, heads, D] of dt with token strides as in
+ * kv_cache_write (all three may be parts of one projection's rows); q_out
+ * [T, Hq, D] contiguous, apart from q.  cos, sin [max_pos, rot/2] fp32, 16-byte
+ * aligned.  positions, slots [T] int32: a token with a negative slot is
+ * skipped, its row of q_out left as it is; so is one with a slot past the
+ * cache or a position outside [0, max_pos), which sets
+ * NVFP4_ERR_DEVICE_INDEX.  The slots of one call must differ.
+ * Hq <= 65535; T*Hq*D and T*heads*D at most 2^34. */
+NVFP4_API nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v,
+                                       nvfp4_dtype dt, int64_t T, int64_t Hq, int64_t q_stride, int64_t k_stride,
+                                       int64_t v_stride, const float* cos, const float* sin, int64_t max_pos,
+                                       int64_t rot, int interleaved, const int32_t* positions, const int32_t* slots,
+                                       void* q_out, nvfp4_stream_t stream);
+
+/* kv_cache_move -- the bytes (codes and scales, keys and values, all heads) of
+ * slot src[m] to slot dst[m], m < M (one launch).
+ * starts [S+1] int32: moves starts[s] .. starts[s+1]-1 belong to sequence s and
+ * take effect one after the other in that order, so accepted drafts can close
+ * up in place; the slots that one sequence writes must not be among another's
+ * slots.  NULL: S == M, every move is a sequence of its own.
+ * A move with a negative src or dst is skipped; one with a slot past the cache
+ * is skipped and sets NVFP4_ERR_DEVICE_INDEX, as does a sequence whose starts
+ * are not 0 <= starts[s] <= starts[s+1] <= M.
+ * S*heads times a row's pieces (up to 34) below 2^31 (beyond:
+ * NVFP4_ERR_UNSUPPORTED). */
+NVFP4_API nvfp4_status kv_cache_move(const nvfp4_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t M,
+                                     const int32_t* starts, int64_t S, nvfp4_stream_t stream);
 
 /* kv_cache_read -- the values of T slots (one launch), exactly as
  * nvfp4_dequantize, mxfp8_dequantize or mxfp4_dequantize give them:
@@ -484,8 +567,26 @@ NVFP4_API nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, 
                                     int64_t max_pages, float scale, int causal, int64_t window, void* out,
                                     float* lse, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
-/* Bytes of workspace with which kv_attention splits as it would choose to,
- * for a cache of `heads` heads of D; 0 when it would not split (or for sizes
+/* kv_attention_tree -- kv_attention for drafted tokens that form trees: the n
+ * queries of a sequence with L = kv_len[b] cached tokens are its last n tokens,
+ * draft d being token L - n + d.  Query i sees draft d iff bit d % 32 of word
+ * d / 32 of its mask is set (bits n and above are ignored; a query sees itself
+ * only where its own bit is set), and the context, j < L - n, whole, or with a
+ * window > 0 where j > L - n + depth - window, depth being the number of drafts
+ * that query i sees less one, and at least 0: with masks of ancestors, the
+ * query's place in its branch.  The window hides no drafts.
+ * tree_mask [T, mask_words] uint32, a row for each query token;
+ * 32*mask_words >= min(max_q, T), mask_words <= 2^20.  q_start is needed.
+ * Everything else, the workspace and its size included, as in kv_attention. */
+NVFP4_API nvfp4_status kv_attention_tree(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt,
+                                         int64_t q_stride, const int32_t* q_start, const int32_t* kv_len,
+                                         const int32_t* page_table, const uint32_t* tree_mask, int64_t mask_words,
+                                         int64_t B, int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv,
+                                         int64_t max_pages, float scale, int64_t window, void* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Bytes of workspace with which kv_attention and kv_attention_tree split as
+ * they would choose to, for a cache of `heads` heads of D; 0 when it would not split (or for sizes
  * it rejects).  Host only. */
 NVFP4_API size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D,
                                              int64_t max_q, int64_t max_kv, int64_t window);

@@ -6,6 +6,13 @@
 //   z_j = scale * q . k_hat_j,  m = max z_j,  P_j = exp(z_j - m),
 //   out = sum_j P_j v_hat_j / sum_j P_j,  lse = m + ln(sum_j P_j);
 // a query that sees nothing gets out = 0 and lse = -inf.
+//
+// Where the queries are drafts that form a tree (AttnArgs::tree), token
+// C + d, C = L - n, is draft d: query i sees it iff bit d of its mask is set,
+// and of the context, j < C, what lies in its window, from its position C +
+// depth on (depth: drafts that it sees besides itself, at least 0).  The
+// kernels are the same: steps that end before C are like any others, and only
+// those with drafts look at the masks.
 #pragma once
 
 #include <type_traits>
@@ -41,6 +48,8 @@ struct AttnArgs {
   float* part_o;                // [chunks, T, Hq, D]; [workers, 2, rows, D]
   int4* part_head;              // k_kv_decode: [workers]
   FastDiv by_page;
+  const uint32_t* tree;         // [T, tree_words] masks over a sequence's drafts, or NULL; then causal is 0
+  uint32_t tree_words;
 };
 
 // A sequence's queries and cached length; false (and the device error word)
@@ -82,6 +91,38 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& a, const Seq& s, uin
   r.lo = a.window ? max(0, p0 - (int32_t)a.window + 1) : 0;
   r.hi = a.causal ? min((int32_t)s.L, p1 + 1) : (int32_t)s.L;
   return r;
+}
+
+// Drafts that form a tree.  A tile's range is that of draft 0: a position is
+// the root's at least.  tree_range: of draft i alone, but for its mask.
+__device__ __forceinline__ const uint32_t* tree_mask(const AttnArgs& a, const Seq& s, uint32_t i) {
+  return a.tree + (uint64_t)(s.t0 + i) * a.tree_words;
+}
+__device__ __forceinline__ Range tree_range(const AttnArgs& a, const Seq& s, uint32_t i) {
+  Range r = tile_range(a, s, 0, 0);
+  if (a.window) {
+    const uint32_t* m = tree_mask(a, s, i);
+    int32_t seen = 0;
+    for (uint32_t w = 0; 32u * w < s.n; ++w) seen += __popc(__ldg(m + w) & (s.n - 32u * w < 32u ? ~(~0u << (s.n - 32u * w)) : ~0u));
+    r.lo = max(0, (int32_t)(s.L - s.n) + min(max(seen - 1, 0) - (int32_t)a.window + 1, 0));  // of the context: drafts go by the mask
+  }
+  return r;
+}
+// What every query of a tile sees whole: none of the drafts, and the context
+// from the deepest possible position's window on.
+__device__ __forceinline__ Range tree_common(const AttnArgs& a, const Seq& s) {
+  Range r;
+  r.lo = a.window ? max(0, (int32_t)(s.L - a.window)) : 0;
+  r.hi = (int32_t)(s.L - s.n);
+  return r;
+}
+// Bits of 32 tokens from j on: drafts as the mask m says, the context ones.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, const Seq& s, const uint32_t* m, int32_t j) {
+  const int32_t d = j - (int32_t)(s.L - s.n);
+  if (d <= -32) return ~0u;
+  if (d < 0) return __ldg(m) << -d | ~(~0u << -d);
+  const uint32_t w = (uint32_t)d >> 5;
+  return __funnelshift_r(w < a.tree_words ? __ldg(m + w) : 0u, w + 1u < a.tree_words ? __ldg(m + w + 1) : 0u, (uint32_t)d & 31u);
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -654,7 +695,9 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <typename QT, int MODE, int DP, int NT, bool EXACT>
+// TREE: the queries are drafts with masks (as a variant of its own: looked up
+// at run time, the masks made the others spill registers).
+template <typename QT, int MODE, int DP, int NT, bool EXACT, bool TREE = false>
 __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant__ AttnArgs a) {
   using D = Decode<QT, MODE, DP, NT, EXACT>;
   using G = Geo<MODE, DP>;
@@ -909,7 +952,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t i = min(r0 + 8u * nt + 2u * d.c + e, R - 1u) / a.G;
-        const Range r = tile_range(a, s, i, i);
+        const Range r = TREE ? tree_range(a, s, i) : tile_range(a, s, i, i);
         see_lo[nt][e] = r.lo;
         see_hi[nt][e] = r.hi;
         d.m[nt][e] = -INFINITY;
@@ -919,7 +962,12 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
       }
     // tokens every row of the tile sees
     const uint32_t i0 = r0 / a.G, i1 = (min(r0 + ROWS, R) - 1u) / a.G;
-    const int32_t all_lo = max(at.w.lo, tile_range(a, s, i1, i1).lo), all_hi = min(at.w.hi, tile_range(a, s, i0, i0).hi);
+    int32_t all_lo = max(at.w.lo, tile_range(a, s, i1, i1).lo), all_hi = min(at.w.hi, tile_range(a, s, i0, i0).hi);
+    if constexpr (TREE) {
+      const Range r = tree_common(a, s);
+      all_lo = max(at.w.lo, r.lo);
+      all_hi = min(at.w.hi, r.hi);
+    }
 
     for (uint32_t k = 0; k < n; ++k, ++it) {
       const uint32_t st = it % ST;
@@ -947,6 +995,17 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
               const int32_t j = j0 + (int32_t)x;
               if (!((there >> x) & 1u) || j < see_lo[nt][e & 1] || j >= see_hi[nt][e & 1]) sv[t][nt][e] = -INFINITY;
             }
+          if (TREE && j0 + 16 * (t + 1) > (int32_t)(s.L - s.n)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t i = min(r0 + 8u * nt + 2u * d.c + e, R - 1u) / a.G;
+                const uint32_t bits = tree_bits(a, s, tree_mask(a, s, i), j0 + 16 * t) >> D::token(d.g);
+                if (!(bits & 1u)) sv[t][nt][e] = -INFINITY;
+                if (!(bits & 256u)) sv[t][nt][2 + e] = -INFINITY;
+              }
+          }
           in[t] = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1177,7 +1236,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const __grid_consta
   // the row tile this query's row was in
   const uint32_t r0 = (i * a.G + h % a.G) / a.tile_rows * a.tile_rows;
   const uint32_t r1 = min(r0 + a.tile_rows, s.n * a.G) - 1u;
-  const Range rg = tile_range(a, s, r0 / a.G, r1 / a.G);
+  const Range rg = tile_range(a, s, a.tree ? 0u : r0 / a.G, r1 / a.G);
   const int32_t span = rg.hi > rg.lo ? rg.hi - (rg.lo & ~15) : 0;
   if (span <= a.chunk) return;  // finished by its CTA
   const uint32_t nc = ((uint32_t)span + a.chunk - 1u) / a.chunk;

@@ -271,7 +271,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-template <typename QT, int MODE, int DP>
+template <typename QT, int MODE, int DP, bool TREE = false>  // TREE: the queries are drafts with masks
 __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant__ AttnArgs a) {
   using S = Shape<MODE, DP>;
   constexpr int NQ = S::NQ, NT = S::NT;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   const uint32_t R = s.n * a.G;
   if (r0 >= R) return;
   const uint32_t rl = min(r0 + 128u * NQ, R) - 1u;
-  const Range rg = tile_range(a, s, r0 / a.G, rl / a.G);
+  const Range rg = tile_range(a, s, TREE ? 0u : r0 / a.G, rl / a.G);
   const int32_t base = rg.lo & ~15;
   const int32_t span = rg.hi > rg.lo ? rg.hi - base : 0;
   if (chunk > 0 && (int64_t)chunk * a.chunk >= span) return;
@@ -493,9 +493,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     const uint32_t tl = tmem + ((32u * ((uint32_t)warp & 3u)) << 16);
     const uint32_t ts_ = tl + S::tm_s + 128u * qt + S::HC * half, to = tl + S::tm_o + 128u * qt;
     const uint32_t i = min(r, R - 1u) / a.G;
-    const Range see = tile_range(a, s, i, i);
+    const Range see = TREE ? tree_range(a, s, i) : tile_range(a, s, i, i);
     const uint32_t f0 = r0 + 128u * qt, f1 = min(f0 + 127u, R - 1u);
-    const int32_t all_lo = tile_range(a, s, f1 / a.G, f1 / a.G).lo, all_hi = min(end, tile_range(a, s, f0 / a.G, f0 / a.G).hi);
+    int32_t all_lo = tile_range(a, s, f1 / a.G, f1 / a.G).lo, all_hi = min(end, tile_range(a, s, f0 / a.G, f0 / a.G).hi);
+    if constexpr (TREE) {
+      const Range all = tree_common(a, s);
+      all_lo = all.lo;
+      all_hi = min(end, all.hi);
+    }
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     auto leave = [&]() {
@@ -521,6 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
           const int32_t jc = j0 + 32 * c;
           const int32_t lo = see.lo - jc, hi = min(see.hi, end) - jc;
           uint32_t in = (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u) & (hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u);
+          if constexpr (TREE) in &= tree_bits(a, s, tree_mask(a, s, i), jc);
           if (any_bad)
             for (int e = 0; e < 32; ++e)
               if (((in >> e) & 1u) && (uint32_t)__ldg(table + a.by_page.div((uint32_t)(jc + e))) >= a.num_pages) in &= ~(1u << e);

@@ -1,0 +1,407 @@
+// Root-mean-square norm in front of a block-scaled product, with the addition
+// of the residual stream, and its gradient.
+//
+// Forward, per row of K elements (T the tensors' type):
+//   h = T(x + residual)          (h = x without a residual)
+//   r = fp32(1 / sqrt(sum_k h_k^2 / K + eps))
+//   y_k = fp32(fp32(h_k r) w_k)
+// and y leaves as T(y), or as the codes and scales that the quantizers
+// (quantize.cuh) give for the fp32 values y.
+// Backward, dy the gradient of y and dh what reaches h past the norm:
+//   s = sum_k w_k dy_k h_k,  dx = T(dh + r (w dy - h r^2 s / K)),
+//   dw_k = sum over rows of dy_k h_k r.
+//
+// The sum of squares and the root are in fp64, so that r is the correctly
+// rounded one but for about 2^-26 of the rows, whatever order the sum is taken
+// in: a step of r moves values across the borders of the 4-bit codes.
+#pragma once
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "quantize.cuh"
+
+namespace nvfp4 {
+namespace norm {
+
+// Modes as in nvfp4_mode, and the plain output.
+enum { kPlain = 3 };
+
+constexpr int kMaxThreads = 512;  // of a CTA; 16 elements a thread and step
+
+struct Args {
+  const void* x;
+  const void* residual;  // or NULL
+  const void* w;
+  void* h;               // or NULL
+  void* y;               // kPlain: T, else codes
+  float* rstd;           // or NULL
+  const float* g;
+  ScaleOut so;
+  int64_t rows;
+  uint32_t K, blocks;    // blocks: K / 16
+  uint32_t row_warps;    // warps a row has; the CTA's other warps take other rows
+  double eps, per_k;     // per_k: 1 / K
+};
+
+struct VjpArgs {
+  const void* dy;
+  const void* h;
+  const void* w;
+  const float* rstd;
+  const void* dh;        // or NULL
+  void* dx;
+  float* dw;             // or NULL
+  float* part;           // [parts, K]
+  uint32_t parts;
+  int64_t rows;
+  uint32_t K, blocks, row_warps;
+};
+
+// A block of 16 elements.  Plain loads, not the read-only path: h may take x's
+// or the residual's place.
+template <typename T, bool V8>
+__device__ __forceinline__ void load_rw(const T* p, RawBlk<T>& r) {
+  constexpr int n = (int)sizeof(r.w) / 16;
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  if constexpr (V8) {
+#pragma unroll
+    for (int i = 0; i < n; i += 2)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r.w[i].x), "=r"(r.w[i].y), "=r"(r.w[i].z), "=r"(r.w[i].w), "=r"(r.w[i + 1].x), "=r"(r.w[i + 1].y),
+                     "=r"(r.w[i + 1].z), "=r"(r.w[i + 1].w)
+                   : "l"(q + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[i].x), "=r"(r.w[i].y), "=r"(r.w[i].z), "=r"(r.w[i].w) : "l"(q + i));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void zero(RawBlk<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(r.w) / 16); ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+}
+// 16 fp32 values rounded to T.
+template <typename T>
+__device__ __forceinline__ void pack16(const float (&v)[16], RawBlk<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+  } else {
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p[i] = std::is_same<T, __half>::value ? pack_f16x2(v[2 * i], v[2 * i + 1]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    r.w[0] = make_uint4(p[0], p[1], p[2], p[3]);
+    r.w[1] = make_uint4(p[4], p[5], p[6], p[7]);
+  }
+}
+template <typename T, bool V8>
+__device__ __forceinline__ void store_blk(T* p, const RawBlk<T>& r) {
+  constexpr int n = (int)sizeof(r.w) / 16;
+  uint4* q = reinterpret_cast<uint4*>(p);
+  if constexpr (V8) {
+#pragma unroll
+    for (int i = 0; i < n; i += 2)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q + i), "r"(r.w[i].x), "r"(r.w[i].y), "r"(r.w[i].z),
+                   "r"(r.w[i].w), "r"(r.w[i + 1].x), "r"(r.w[i + 1].y), "r"(r.w[i + 1].z), "r"(r.w[i + 1].w)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) q[i] = r.w[i];
+  }
+}
+
+// A row's sum over its warps' lanes, the same bits in all of them; `red` has
+// a place for each warp, two buffers in turn (one barrier a row).
+template <typename F>
+__device__ __forceinline__ F row_sum(F v, F* red, uint32_t row_warps, uint32_t first) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (row_warps == 1) return v;
+  if ((threadIdx.x & 31u) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[first];
+  for (uint32_t i = 1; i < row_warps; ++i) v += red[first + i];
+  return v;
+}
+
+// Codes and scale byte of this lane's 16 fp32 values (MX: of the lane pair's
+// 32); all lanes call it.
+template <int OUT>
+__device__ __forceinline__ uint32_t encode(const float (&v)[16], float E, uint4& q) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+  uint32_t s;
+  if constexpr (OUT == kv::kNV) {
+    float t = m / kE2M1Max;
+    t = t * E;
+    s = f32_to_e4m3(t);
+    const float fs = e4m3_to_f32(s);
+    const float k = fs != 0.0f ? E / fs : 0.0f;
+    q.x = s != 0u ? scaled_e2m1x8_at(v, 0, k) : 0u;  // a zero scale stores zero codes
+    q.y = s != 0u ? scaled_e2m1x8_at(v, 8, k) : 0u;
+  } else {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    s = f32_to_ue8m0_rp(m / (OUT == kv::kMX8 ? kE4M3Max : kE2M1Max));
+    const float k = 1.0f / ue8m0_to_f32(s);
+    if constexpr (OUT == kv::kMX8) {
+      q.x = f32x4_to_e4m3x4(v[0] * k, v[1] * k, v[2] * k, v[3] * k);
+      q.y = f32x4_to_e4m3x4(v[4] * k, v[5] * k, v[6] * k, v[7] * k);
+      q.z = f32x4_to_e4m3x4(v[8] * k, v[9] * k, v[10] * k, v[11] * k);
+      q.w = f32x4_to_e4m3x4(v[12] * k, v[13] * k, v[14] * k, v[15] * k);
+    } else {
+      q.x = scaled_e2m1x8_at(v, 0, k);
+      q.y = scaled_e2m1x8_at(v, 8, k);
+    }
+  }
+  return s;
+}
+
+// Scale bytes of the blocks that a warp's lanes hold, four to a store where
+// they lie together.  b: this lane's 16-element block, n of them in a row;
+// b's remainder by 32 is the lane.  All lanes call it.
+template <int OUT>
+__device__ __forceinline__ void put_scales(const ScaleOut& so, uint32_t row, uint32_t b, uint32_t n, uint32_t s) {
+  constexpr uint32_t per = OUT == kv::kNV ? 1 : 2;  // lanes a scale
+  const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, per), s2 = __shfl_down_sync(0xffffffffu, s, 2 * per),
+                 s3 = __shfl_down_sync(0xffffffffu, s, 3 * per);
+  const uint32_t c = b / per, cols = so.blocks_per_row, c0 = c & ~3u;
+  if (b >= n || b % per) return;
+  const bool four = c0 + 4u <= cols && (so.swizzled || cols % 4u == 0);
+  if (four && c != c0) return;
+  uint8_t* to = so.p + (so.swizzled ? (size_t)swizzled_offset(row, c, so.Cp) : (size_t)row * cols + c);
+  if (four) *reinterpret_cast<uint32_t*>(to) = __byte_perm(s | (s1 << 8), s2 | (s3 << 8), 0x5410);
+  else *to = (uint8_t)s;
+}
+
+// U: 16-element blocks a thread has.  With one, loads and stores are of 32
+// bytes, the weights stay in registers and the next row's loads are in flight
+// while this row is summed and stored; with four (long rows, and rows that are
+// not 32-byte aligned) that would spill.
+template <typename T, int OUT, int U>
+__global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant__ Args a) {
+  constexpr bool kAhead = U == 1, V8 = U == 1;
+  __shared__ double red[2][kMaxThreads / 32];
+  const uint32_t warp = threadIdx.x >> 5, rpc = (blockDim.x >> 5) / a.row_warps;  // rows a CTA
+  const uint32_t mine = warp / a.row_warps, first = mine * a.row_warps, span = a.row_warps * 32u;
+  const uint32_t b0 = threadIdx.x - first * 32u;  // this thread's blocks: b0 + span u
+  const float E = OUT == kv::kNV && a.g ? kGlobalEncode / __ldg(a.g) : 1.0f;
+  const T* w = static_cast<const T*>(a.w);
+  RawBlk<T> h[U], res, wr;
+  auto load = [&](int64_t row, int u) {
+    const uint32_t b = b0 + span * u;
+    if (row < a.rows && b < a.blocks) {
+      const int64_t at = row * a.K + (int64_t)b * 16;
+      load_rw<T, V8>(static_cast<const T*>(a.x) + at, h[u]);
+      if (a.residual) load_rw<T, V8>(static_cast<const T*>(a.residual) + at, res);
+    } else {
+      zero(h[u]);
+      zero(res);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * rpc;
+  int64_t row = (int64_t)blockIdx.x * rpc + mine;
+  if constexpr (kAhead) {
+    load(row, 0);
+    if (b0 < a.blocks) load_blk<T, V8>(w + b0 * 16u, wr);
+    else zero(wr);
+  }
+  uint32_t turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * rpc; base < a.rows; base += step, row += step, turn ^= 1u) {
+    double sum = 0.0;
+    RawBlk<T> cur;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!kAhead) load(row, u);
+      float v[16];
+      unpack16<T>(h[u], v);
+      if (a.residual) {
+        float c[16];
+        unpack16<T>(res, c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += c[i];
+        pack16<T>(v, h[u]);
+        unpack16<T>(h[u], v);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const double d = (double)v[i];
+        sum = fma(d, d, sum);
+      }
+      const uint32_t b = b0 + span * u;
+      if (a.h && row < a.rows && b < a.blocks) store_blk<T, V8>(static_cast<T*>(a.h) + row * a.K + (int64_t)b * 16, h[u]);
+    }
+    if constexpr (kAhead) {
+      cur = h[0];
+      load(row + step, 0);
+    }
+    sum = row_sum(sum, red[turn], a.row_warps, first);
+    const float r = (float)rsqrt(fma(sum, a.per_k, a.eps));
+    if (a.rstd && b0 == 0 && row < a.rows) a.rstd[row] = r;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = b0 + span * u;
+      const bool in = row < a.rows && b < a.blocks;
+      float v[16], c[16];
+      if constexpr (kAhead) {
+        unpack16<T>(cur, v);
+      } else {
+        unpack16<T>(h[u], v);
+        if (b < a.blocks) load_blk<T, V8>(w + b * 16u, wr);
+        else zero(wr);
+      }
+      unpack16<T>(wr, c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = (v[i] * r) * c[i];
+      if constexpr (OUT == kPlain) {
+        RawBlk<T> y;
+        pack16<T>(v, y);
+        if (in) store_blk<T, V8>(static_cast<T*>(a.y) + row * a.K + (int64_t)b * 16, y);
+      } else {
+        uint4 q;
+        const uint32_t s = encode<OUT>(v, E, q);
+        if (in) {
+          const int64_t at = row * a.blocks + b;
+          if constexpr (OUT == kv::kMX8) static_cast<uint4*>(a.y)[at] = q;
+          else static_cast<uint2*>(a.y)[at] = make_uint2(q.x, q.y);
+        }
+        put_scales<OUT>(a.so, (uint32_t)row, b, row < a.rows ? a.blocks : 0u, s);
+      }
+    }
+  }
+  if constexpr (OUT != kPlain) zero_scale_padding(a.so, (uint32_t)a.rows);
+}
+
+// The parts of dw stay in registers over all rows of a CTA; dy and h do over a
+// row where they fit beside them (HOLD), and are read twice elsewhere.
+template <typename T, int U>
+__global__ void __launch_bounds__(kMaxThreads) k_rms_norm_vjp(const __grid_constant__ VjpArgs a) {
+  constexpr bool HOLD = U == 1, V8 = U == 1;
+  __shared__ float red[2][kMaxThreads / 32];
+  const uint32_t warp = threadIdx.x >> 5, rpc = (blockDim.x >> 5) / a.row_warps;
+  const uint32_t mine = warp / a.row_warps, first = mine * a.row_warps, span = a.row_warps * 32u;
+  const uint32_t b0 = threadIdx.x - first * 32u;
+  const T* w = static_cast<const T*>(a.w);
+  constexpr int N = HOLD ? U : 1;
+  RawBlk<T> dy[N], h[N], wr[N], dh;
+  float acc[U][16];
+  auto load_w = [&](int u) {
+    const uint32_t b = b0 + span * u;
+    if (b < a.blocks) load_blk<T, V8>(w + b * 16u, wr[u % N]);
+    else zero(wr[u % N]);
+  };
+  auto load = [&](int64_t row, int u) {
+    const uint32_t b = b0 + span * u;
+    if (row < a.rows && b < a.blocks) {
+      const int64_t at = row * a.K + (int64_t)b * 16;
+      load_rw<T, V8>(static_cast<const T*>(a.dy) + at, dy[u % N]);
+      load_rw<T, V8>(static_cast<const T*>(a.h) + at, h[u % N]);
+    } else {
+      zero(dy[u % N]);
+      zero(h[u % N]);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if constexpr (HOLD) load_w(u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * rpc;
+  int64_t row = (int64_t)blockIdx.x * rpc + mine;
+  uint32_t turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * rpc; base < a.rows; base += step, row += step, turn ^= 1u) {
+    const float r = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
+    float s = 0.0f;
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(row, u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!HOLD) {
+        load(row, u);
+        load_w(u);
+      }
+      float d[16], x[16], c[16];
+      unpack16<T>(dy[u % N], d);
+      unpack16<T>(h[u % N], x);
+      unpack16<T>(wr[u % N], c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s = fmaf(d[i] * c[i], x[i], s);
+        acc[u][i] = fmaf(d[i], x[i] * r, acc[u][i]);
+      }
+    }
+    s = row_sum(s, red[turn], a.row_warps, first);
+    const float f = s / (float)a.K * r * r;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = b0 + span * u;
+      const bool in = row < a.rows && b < a.blocks;
+      if constexpr (!HOLD) {
+        load(row, u);
+        load_w(u);
+      }
+      const int64_t at = row * a.K + (int64_t)b * 16;
+      if (a.dh && in) load_rw<T, V8>(static_cast<const T*>(a.dh) + at, dh);
+      else zero(dh);
+      float d[16], x[16], c[16];
+      unpack16<T>(dy[u % N], d);
+      unpack16<T>(h[u % N], x);
+      unpack16<T>(wr[u % N], c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(-x[i], f, d[i] * c[i]);
+      unpack16<T>(dh, c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], r, c[i]);
+      RawBlk<T> y;
+      pack16<T>(x, y);
+      if (in) store_blk<T, V8>(static_cast<T*>(a.dx) + at, y);
+    }
+  }
+  if (!a.dw) return;
+  float* part = a.part + ((uint64_t)blockIdx.x * rpc + mine) * a.K;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t b = b0 + span * u;
+    if (b >= a.blocks) continue;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<float4*>(part + b * 16u + i) = make_float4(acc[u][i], acc[u][i + 1], acc[u][i + 2], acc[u][i + 3]);
+  }
+}
+
+// dw: the parts added up, 32 columns a CTA (8 lanes of 4) by 32 groups of
+// parts, each group's sum in order and the groups' in order.
+__global__ void __launch_bounds__(256) k_rms_norm_dw(const __grid_constant__ VjpArgs a) {
+  __shared__ float4 sum[32][8];
+  const uint32_t c = threadIdx.x & 7u, grp = threadIdx.x >> 3, col = blockIdx.x * 32u + c * 4u;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < a.K)
+#pragma unroll 4
+    for (uint32_t p = grp; p < a.parts; p += 32u) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part + (uint64_t)p * a.K + col);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  sum[grp][c] = s;
+  __syncthreads();
+  if (grp != 0 || col >= a.K) return;
+  for (uint32_t i = 1; i < 32u; ++i) {
+    const float4 v = sum[i][c];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  *reinterpret_cast<float4*>(a.dw + col) = s;
+}
+
+}  // namespace norm
+}  // namespace nvfp4

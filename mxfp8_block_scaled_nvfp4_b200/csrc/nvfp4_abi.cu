@@ -19,8 +19,10 @@
 #include "qqmm_sm100.cuh"
 #include "gather_qmm.cuh"
 #include "kv_cache.cuh"
+#include "kv_append.cuh"
 #include "kv_attention.cuh"
 #include "kv_prefill.cuh"
+#include "norm.cuh"
 
 using namespace nvfp4;
 
@@ -93,25 +95,26 @@ nvfp4_status device_info(const char* tag, DeviceInfo* out) {
   return NVFP4_OK;
 }
 
+int64_t dt_size(nvfp4_dtype dt) { return dt == NVFP4_DT_F32 ? 4 : 2; }
+
 bool valid_dt(nvfp4_dtype dt) { return dt == NVFP4_DT_F32 || dt == NVFP4_DT_F16 || dt == NVFP4_DT_BF16; }
 
 // CTAs of `fn` (threads per CTA, dynamic shared memory) that fit on one SM
-// at once, cached per kernel.
+// at once, cached per kernel and CTA size.
 int resident_ctas(const void* fn, int threads, size_t smem) {
+  struct Known {
+    const void* fn;
+    int threads, ctas;
+  };
   static std::mutex mu;
-  static const void* keys[128];
-  static int vals[128];
+  static Known known[512];
   static int n = 0;
   std::lock_guard<std::mutex> lk(mu);
   for (int i = 0; i < n; ++i)
-    if (keys[i] == fn) return vals[i];
+    if (known[i].fn == fn && known[i].threads == threads) return known[i].ctas;
   int b = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, smem) != cudaSuccess || b < 1) b = 1;
-  if (n < 128) {
-    keys[n] = fn;
-    vals[n] = b;
-    ++n;
-  }
+  if (n < 512) known[n++] = Known{fn, threads, b};
   return b;
 }
 
@@ -144,6 +147,28 @@ void dispatch_mode(nvfp4_mode mode, F&& f) {
 }
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;  // 16 Gi elements: 32-bit half-block indices
+
+// How a norm kernel lays a row of `blocks` 16-element blocks over a CTA: one
+// block a thread where the rows are 32-byte aligned and fit (K <= 8192), else
+// four; row_warps warps a row, `warps` a CTA (as many rows as make about eight).
+struct NormPlan {
+  bool one;
+  uint32_t row_warps, warps;
+};
+NormPlan norm_plan(int64_t blocks, bool aligned) {
+  NormPlan p;
+  p.one = aligned && blocks <= norm::kMaxThreads;
+  const int64_t per_warp = p.one ? 32 : 128;
+  p.row_warps = (uint32_t)((blocks + per_warp - 1) / per_warp);
+  p.warps = p.row_warps >= 8 ? p.row_warps : 8 / p.row_warps * p.row_warps;
+  return p;
+}
+template <typename F>
+void dispatch_norm(const NormPlan& p, F&& f) {
+  if (p.one) f(std::integral_constant<int, 1>{});
+  else f(std::integral_constant<int, 4>{});
+}
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 }  // namespace
 
@@ -810,6 +835,162 @@ nvfp4_status gather_qmm_noalloc(const void* x, const uint32_t* w_codes, const ui
   return gather_qmm(x, w_codes, w_scales, g, idx, T, topk, E, N, K, y, scratch, kNoAllocScratchBytes, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Root-mean-square norm
+// ---------------------------------------------------------------------------
+constexpr int64_t kNormMaxK = 32768;
+
+static nvfp4_status check_norm(const char* tag, nvfp4_dtype dt, int64_t rows, int64_t K, int64_t group) {
+  if (!valid_dt(dt)) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] dtype must be float32, float16 or bfloat16", tag);
+  if (rows < 0 || K < 0 || product_exceeds(rows, K, kMaxElems))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad shape [%lld, %lld]", tag, (long long)rows, (long long)K);
+  if (K < group || K % group != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] K must be a positive multiple of %lld, got %lld", tag, (long long)group, (long long)K);
+  if (K > kNormMaxK)
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] K must be at most %lld, got %lld", tag, (long long)kNormMaxK, (long long)K);
+  return NVFP4_OK;
+}
+
+// mode: nvfp4_mode or norm::kPlain.
+static nvfp4_status rms_norm_launch(const char* tag, int mode, const void* x, const void* residual, const void* w,
+                                    nvfp4_dtype dt, int64_t rows, int64_t K, double eps, const float* g, void* h,
+                                    void* y, uint8_t* scales, nvfp4_layout layout, float* rstd, nvfp4_stream_t stream) {
+  const int64_t group = mode == kv::kMX8 || mode == kv::kMX4 ? 32 : 16;
+  nvfp4_status st = check_norm(tag, dt, rows, K, group);
+  if (st != NVFP4_OK) return st;
+  if (layout != NVFP4_LAYOUT_LINEAR && layout != NVFP4_LAYOUT_SWIZZLED)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] unknown scale layout", tag);
+  if (g && mode != kv::kNV) return fail(NVFP4_ERR_INVALID_ARG, "[%s] Global scales are only supported for 'nvfp4' mode.", tag);
+  if (!(eps >= 0x1p-126 && eps <= 0x1p126))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] eps must be in [2^-126, 2^126], got %g", tag, eps);
+  if (rows > 0 && (!x || !w || !y || (mode != norm::kPlain && !scales))) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (rows > 0 && (residual == nullptr) != (h == nullptr))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] h must be given with a residual, and only then", tag);
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(y) || !aligned16(scales) ||
+      (reinterpret_cast<uintptr_t>(g) & 3u) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned (g and rstd 4-byte)", tag);
+  if (rows == 0) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  norm::Args a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.residual = residual;
+  a.w = w;
+  a.h = h;
+  a.y = y;
+  a.rstd = rstd;
+  a.g = g;
+  if (mode != norm::kPlain) a.so = scale_out(scales, K, (int)group, layout);
+  a.rows = rows;
+  a.K = (uint32_t)K;
+  a.blocks = (uint32_t)(K / 16);
+  a.eps = eps;
+  a.per_k = 1.0 / (double)K;
+  const bool v8 = aligned32(x) && aligned32(residual) && aligned32(w) && aligned32(h) && (mode != norm::kPlain || aligned32(y)) &&
+                  K * dt_size(dt) % 32 == 0;
+  const NormPlan p = norm_plan(a.blocks, v8);
+  a.row_warps = p.row_warps;
+  const int64_t rpc = p.warps / p.row_warps, want = (rows + rpc - 1) / rpc;
+  dispatch_dt(dt, [&](auto tag_t) {
+    using T = decltype(tag_t);
+    dispatch_norm(p, [&](auto u) {
+      constexpr int U = decltype(u)::value;
+      auto go = [&](auto kern) {
+        const int64_t cap = (int64_t)d.sm_count * resident_ctas((const void*)kern, (int)p.warps * 32, 0);
+        kern<<<(unsigned)(want < cap ? want : cap), p.warps * 32u, 0, stream>>>(a);
+      };
+      if (mode == kv::kNV) go(norm::k_rms_norm<T, kv::kNV, U>);
+      else if (mode == kv::kMX8) go(norm::k_rms_norm<T, kv::kMX8, U>);
+      else if (mode == kv::kMX4) go(norm::k_rms_norm<T, kv::kMX4, U>);
+      else go(norm::k_rms_norm<T, norm::kPlain, U>);
+    });
+  });
+  return check_launch(tag);
+}
+
+nvfp4_status rms_norm(const void* x, const void* residual, const void* w, nvfp4_dtype dt, int64_t rows, int64_t K,
+                      double eps, void* h, void* y, float* rstd, nvfp4_stream_t stream) {
+  return rms_norm_launch("rms_norm", norm::kPlain, x, residual, w, dt, rows, K, eps, nullptr, h, y, nullptr,
+                         NVFP4_LAYOUT_LINEAR, rstd, stream);
+}
+
+nvfp4_status rms_norm_quantize(nvfp4_mode mode, const void* x, const void* residual, const void* w, nvfp4_dtype dt,
+                               int64_t rows, int64_t K, double eps, const float* g, void* h, uint32_t* codes,
+                               uint8_t* scales, nvfp4_layout layout, float* rstd, nvfp4_stream_t stream) {
+  const char* tag = "rms_norm_quantize";
+  if (mode != NVFP4_MODE_NVFP4 && mode != NVFP4_MODE_MXFP8 && mode != NVFP4_MODE_MXFP4)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] mode must be 'nvfp4', 'mxfp8' or 'mxfp4'", tag);
+  return rms_norm_launch(tag, mode, x, residual, w, dt, rows, K, eps, g, h, codes, scales, layout, rstd, stream);
+}
+
+// CTAs of k_rms_norm_vjp, and parts of dw (one for each row that a CTA takes
+// at a time).
+constexpr int64_t kNormVjpCtas = 148 * 2;
+static int64_t norm_vjp_ctas(const NormPlan& p, int64_t rows) {
+  const int64_t rpc = p.warps / p.row_warps, want = (rows + rpc - 1) / rpc;
+  return want < kNormVjpCtas ? want : kNormVjpCtas;
+}
+
+size_t rms_norm_vjp_workspace_size(int64_t rows, int64_t K) {
+  if (rows < 1 || K < 16 || K % 16 != 0 || K > kNormMaxK || product_exceeds(rows, K, kMaxElems)) return 0;
+  size_t most = 0;
+  for (int v8 = 0; v8 < 2; ++v8) {
+    const NormPlan p = norm_plan(K / 16, v8 != 0);
+    const size_t bytes = (size_t)norm_vjp_ctas(p, rows) * (p.warps / p.row_warps) * (size_t)K * 4;
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
+nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                          nvfp4_dtype dt, int64_t rows, int64_t K, void* dx, float* dw, void* workspace,
+                          size_t workspace_bytes, nvfp4_stream_t stream) {
+  const char* tag = "rms_norm_vjp";
+  nvfp4_status st = check_norm(tag, dt, rows, K, 16);
+  if (st != NVFP4_OK) return st;
+  if (rows > 0 && (!dy || !h || !w || !rstd || !dx)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(w) || !aligned16(dh) || !aligned16(dx) || !aligned16(dw) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned (rstd 4-byte)", tag);
+  if (dw && (workspace_bytes < rms_norm_vjp_workspace_size(rows, K) || (rows > 0 && !workspace)))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] dw needs a workspace of %zu bytes, got %zu", tag,
+                rms_norm_vjp_workspace_size(rows, K), workspace_bytes);
+  if (rows == 0 && !dw) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  norm::VjpArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dy = dy;
+  a.h = h;
+  a.w = w;
+  a.rstd = rstd;
+  a.dh = dh;
+  a.dx = dx;
+  a.dw = dw;
+  a.part = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.K = (uint32_t)K;
+  a.blocks = (uint32_t)(K / 16);
+  if (rows > 0) {
+    const bool v8 = aligned32(dy) && aligned32(h) && aligned32(w) && aligned32(dh) && aligned32(dx) && K * dt_size(dt) % 32 == 0;
+    const NormPlan p = norm_plan(a.blocks, v8);
+    a.row_warps = p.row_warps;
+    const int64_t ctas = norm_vjp_ctas(p, rows);
+    a.parts = (uint32_t)(ctas * (p.warps / p.row_warps));
+    dispatch_dt(dt, [&](auto tag_t) {
+      using T = decltype(tag_t);
+      dispatch_norm(p, [&](auto u) {
+        norm::k_rms_norm_vjp<T, decltype(u)::value><<<(unsigned)ctas, p.warps * 32u, 0, stream>>>(a);
+      });
+    });
+  }
+  if (dw) norm::k_rms_norm_dw<<<(unsigned)((K + 31) / 32), 256, 0, stream>>>(a);
+  return check_launch(tag);
+}
+
 // Checks of a cache handle that every cache call makes.
 static nvfp4_status check_kv_cache(const char* tag, const nvfp4_kv_cache* c) {
   if (!c) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null cache", tag);
@@ -835,8 +1016,6 @@ static nvfp4_status check_kv_cache(const char* tag, const nvfp4_kv_cache* c) {
     return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned", tag);
   return NVFP4_OK;
 }
-
-static int64_t dt_size(nvfp4_dtype dt) { return dt == NVFP4_DT_F32 ? 4 : 2; }
 
 // Token stride of a [T, width] operand whose rows may be parts of longer ones.
 static bool bad_stride(int64_t T, int64_t stride, int64_t width, nvfp4_dtype dt) {
@@ -937,6 +1116,113 @@ nvfp4_status kv_cache_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
   return check_launch(tag);
 }
 
+nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* q, const void* k, const void* v, nvfp4_dtype dt,
+                             int64_t T, int64_t Hq, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const float* cos, const float* sin, int64_t max_pos, int64_t rot, int interleaved,
+                             const int32_t* positions, const int32_t* slots, void* q_out, nvfp4_stream_t stream) {
+  const char* tag = "kv_cache_append";
+  nvfp4_status st = check_kv_cache(tag, cache);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dt(dt)) return fail(NVFP4_ERR_UNSUPPORTED, "[%s] dtype must be float32, float16 or bfloat16", tag);
+  if (Hq < 1 || Hq > 65535) return fail(NVFP4_ERR_INVALID_ARG, "[%s] Hq must be in [1, 65535], got %lld", tag, (long long)Hq);
+  const int64_t width = cache->heads * cache->D, q_width = Hq * cache->D;
+  if (T < 0 || product_exceeds(T, width, kMaxElems) || product_exceeds(T, q_width, kMaxElems))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad T=%lld", tag, (long long)T);
+  if (rot < 16 || rot > cache->D || rot % 16 != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] rot must be a multiple of 16 in [16, D], got %lld", tag, (long long)rot);
+  if (max_pos < 0 || max_pos > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad max_pos=%lld", tag, (long long)max_pos);
+  if (bad_stride(T, q_stride, q_width, dt) || bad_stride(T, k_stride, width, dt) || bad_stride(T, v_stride, width, dt))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] token strides must be at least a token's elements and a multiple of 16 bytes", tag);
+  if (T > 0 && (!q || !k || !v || !positions || !slots || !q_out || (max_pos > 0 && (!cos || !sin))))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos) || !aligned16(sin) || !aligned16(q_out) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] tensor pointers must be 16-byte aligned (positions and slots 4-byte)", tag);
+  if (T == 0) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  kv::AppendArgs a;
+  memset(&a, 0, sizeof(a));
+  a.r = kv_row_args(cache, T, slots);
+  a.r.x[0] = k;
+  a.r.x[1] = v;
+  a.r.stride[0] = k_stride;
+  a.r.stride[1] = v_stride;
+  a.q = q;
+  a.q_out = q_out;
+  a.q_stride = q_stride;
+  a.cs[0] = cos;
+  a.cs[1] = sin;
+  a.positions = positions;
+  a.max_pos = (uint32_t)max_pos;
+  a.rot = (uint32_t)rot;
+  a.interleaved = interleaved != 0;
+  a.q_units = (uint32_t)(T * q_width / 16);
+  a.q_per_token.init((uint32_t)(q_width / 16));
+  a.q_ctas = (a.q_units + kv::kRowThreads - 1) / kv::kRowThreads;
+  a.kv_ctas = (a.r.units + kv::kRowThreads - 1) / kv::kRowThreads;
+  const bool v8 = rows_aligned32(q, T, q_stride, dt) && rows_aligned32(k, T, k_stride, dt) && rows_aligned32(v, T, v_stride, dt) &&
+                  aligned32(q_out);
+  dispatch_dt(dt, [&](auto tag_t) {
+    using E = decltype(tag_t);
+    dispatch_mode(cache->mode, [&](auto m) {
+      constexpr int MODE = decltype(m)::value;
+      const unsigned grid = a.q_ctas + 2u * a.kv_ctas;
+      if (v8) kv::k_kv_append<E, MODE, true><<<grid, kv::kRowThreads, 0, stream>>>(a);
+      else kv::k_kv_append<E, MODE, false><<<grid, kv::kRowThreads, 0, stream>>>(a);
+    });
+  });
+  return check_launch(tag);
+}
+
+nvfp4_status kv_cache_move(const nvfp4_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t M,
+                           const int32_t* starts, int64_t S, nvfp4_stream_t stream) {
+  const char* tag = "kv_cache_move";
+  nvfp4_status st = check_kv_cache(tag, cache);
+  if (st != NVFP4_OK) return st;
+  if (M < 0 || M > INT32_MAX || S < 0 || S > INT32_MAX || (!starts && S != M))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] bad M=%lld, S=%lld (without starts, S must equal M)", tag, (long long)M, (long long)S);
+  const int64_t blocks = cache->D / (cache->mode == NVFP4_MODE_NVFP4 ? 16 : 32);
+  const int64_t code_bytes = cache->D / (cache->mode == NVFP4_MODE_MXFP8 ? 1 : 2);
+  const int64_t piece = blocks & -blocks;  // the largest power of two that divides a row's scale bytes: 1 to 16
+  const int64_t pieces = 2 * (code_bytes / 16 + blocks / piece);
+  if (product_exceeds(S, cache->heads * pieces, INT32_MAX))
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] S*heads*%lld must be below 2^31", tag, (long long)pieces);
+  if (M > 0 && (!src || !dst)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
+  if ((reinterpret_cast<uintptr_t>(src) & 3u) || (reinterpret_cast<uintptr_t>(dst) & 3u) || (reinterpret_cast<uintptr_t>(starts) & 3u))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] src, dst and starts must be 4-byte aligned", tag);
+  if (M == 0 || S == 0) return ok();
+  DeviceInfo d;
+  st = device_info(tag, &d);
+  if (st != NVFP4_OK) return st;
+  kv::MoveArgs a;
+  memset(&a, 0, sizeof(a));
+  a.codes[0] = reinterpret_cast<uint8_t*>(cache->k_codes);
+  a.codes[1] = reinterpret_cast<uint8_t*>(cache->v_codes);
+  a.scales[0] = cache->k_scales;
+  a.scales[1] = cache->v_scales;
+  a.src = src;
+  a.dst = dst;
+  a.starts = starts;
+  a.M = (uint32_t)M;
+  a.S = (uint32_t)S;
+  a.heads = (uint32_t)cache->heads;
+  a.page_size = (uint32_t)cache->page_size;
+  a.num_slots = (uint32_t)(cache->num_pages * cache->page_size);
+  a.row[0] = (uint32_t)code_bytes;
+  a.row[1] = (uint32_t)blocks;
+  a.piece = (uint32_t)piece;
+  a.code_pieces = (uint32_t)(code_bytes / 16);
+  a.pieces = (uint32_t)pieces;
+  a.units = (uint32_t)(S * cache->heads * pieces);
+  a.per_seq.init((uint32_t)(cache->heads * pieces));
+  a.per_head.init((uint32_t)pieces);
+  a.by_page.init(a.page_size);
+  kv::k_kv_move<<<(a.units + kv::kRowThreads - 1) / kv::kRowThreads, kv::kRowThreads, 0, stream>>>(a);
+  return check_launch(tag);
+}
+
 // How kv_attention cuts its work.  k_kv_prefill: rows of queries a CTA holds,
 // tokens a CTA walks and the largest number of such chunks a row tile can
 // have.  k_kv_decode: rows of a tile; its CTAs share out the rest themselves.
@@ -947,7 +1233,7 @@ struct KvPlan {
 };
 constexpr int64_t kKvMaxWorkers = 148 * 4, kKvWorkers = 148;  // most, and fewest worth splitting over
 static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
-                      int64_t window, bool prefill_has_it, size_t workspace_bytes) {
+                      int64_t window, bool prefill_has_it, bool tree, size_t workspace_bytes) {
   KvPlan p;
   if (max_q > T) max_q = T;
   const int64_t rows = max_q * (Hq / heads);
@@ -964,7 +1250,10 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   p.prefill = prefill_has_it && rows > (D <= 64 ? 48 : D <= 128 ? 32 : 16);
   p.chunk = p.chunks = 1;
   if (!p.prefill) {
-    p.tile_rows = rows <= 8 || D > 128 ? 8 : 16;  // D 256: two n-tiles would take more registers than there are
+    // D 256: two n-tiles would take more registers than there are; trees of so
+    // few rows are rare and have no variant of their own (the workspace of 8-row
+    // tiles then has room for two workers an SM, as many as are resident)
+    p.tile_rows = (rows <= 8 && !tree) || D > 128 ? 8 : 16;
     p.bytes_per_chunk = (size_t)(2 * p.tile_rows * (D * 4 + 8) + 32);
     return p;
   }
@@ -993,7 +1282,7 @@ size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t hea
     return 0;
   size_t most = 0;  // over the kernels that the types may choose
   for (int i = 0; i < 2; ++i) {
-    const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, SIZE_MAX);
+    const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, false, SIZE_MAX);
     // 64 tokens are one unit of work: nothing to split
     const size_t bytes = p.prefill ? (p.chunks > 1 ? p.chunks * p.bytes_per_chunk : 0)
                                    : (max_kv > 64 ? (size_t)kKvMaxWorkers * p.bytes_per_chunk : 0);
@@ -1002,12 +1291,12 @@ size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t hea
   return most;
 }
 
-nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
-                          const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int64_t B,
-                          int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv, int64_t max_pages, float scale,
-                          int causal, int64_t window, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                          nvfp4_stream_t stream) {
-  const char* tag = "kv_attention";
+// kv_attention, and with masks over the queries' own tokens kv_attention_tree.
+static nvfp4_status kv_attend(const char* tag, const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt,
+                              int64_t q_stride, const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                              int64_t B, int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv, int64_t max_pages,
+                              float scale, int causal, int64_t window, const uint32_t* tree, int64_t tree_words, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
   nvfp4_status st = check_kv_cache(tag, cache);
   if (st != NVFP4_OK) return st;
   if (q_dt != NVFP4_DT_F16 && q_dt != NVFP4_DT_BF16)
@@ -1072,12 +1361,14 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   a.page_size = (uint32_t)cache->page_size;
   a.window = window > (1 << 30) ? 0u : (uint32_t)window;  // a window past any length hides nothing
   a.causal = causal != 0;
+  a.tree = tree;
+  a.tree_words = (uint32_t)tree_words;
   a.scale_bytes = (uint64_t)cache->num_pages * cache->heads * cache->page_size * (cache->D / (cache->mode == NVFP4_MODE_NVFP4 ? 16 : 32));
   a.by_page.init(a.page_size);
   // k_kv_prefill: no two-term Q for fp16 over the MX modes; it copies some row
   // for every token, so there has to be one
   const bool prefill_has_it = (cache->mode == NVFP4_MODE_NVFP4 || q_dt == NVFP4_DT_BF16) && cache->num_pages > 0;
-  const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, prefill_has_it, workspace_bytes);
+  const KvPlan p = kv_plan(B, T, Hq, cache->heads, cache->D, max_q, max_kv, a.window, prefill_has_it, tree != nullptr, workspace_bytes);
   a.chunk = (int32_t)p.chunk;
   a.chunks = (uint32_t)p.chunks;
   a.tile_rows = (uint32_t)p.tile_rows;
@@ -1130,7 +1421,7 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
         constexpr int DP = decltype(dp)::value;
         if (p.prefill) {
           if constexpr (MODE == kv::kNV || std::is_same<QT, __nv_bfloat16>::value) {
-            auto kern = kv::pf::k_kv_prefill<QT, MODE, DP>;
+            auto kern = a.tree ? kv::pf::k_kv_prefill<QT, MODE, DP, true> : kv::pf::k_kv_prefill<QT, MODE, DP>;
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv::pf::Shape<MODE, DP>::smem);
             if (e != cudaSuccess) return;
             kern<<<(unsigned)(tiles * p.chunks * B * cache->heads), kv::pf::THREADS, kv::pf::Shape<MODE, DP>::smem, stream>>>(a);
@@ -1143,11 +1434,18 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
         if constexpr (DP <= 128) {
           if (p.tile_rows == 16) {
             const std::integral_constant<int, 16> r;
-            exact ? decode(kv::k_kv_decode<QT, MODE, DP, 2, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 2, false>, r, smem);
+            if (a.tree) exact ? decode(kv::k_kv_decode<QT, MODE, DP, 2, true, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 2, false, true>, r, smem);
+            else exact ? decode(kv::k_kv_decode<QT, MODE, DP, 2, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 2, false>, r, smem);
             return;
           }
         }
         const std::integral_constant<int, 8> r;
+        if constexpr (DP > 128) {
+          if (a.tree) {
+            exact ? decode(kv::k_kv_decode<QT, MODE, DP, 1, true, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 1, false, true>, r, smem);
+            return;
+          }
+        }
         exact ? decode(kv::k_kv_decode<QT, MODE, DP, 1, true>, r, smem) : decode(kv::k_kv_decode<QT, MODE, DP, 1, false>, r, smem);
       };
       if (a.D <= 64) with_dim(std::integral_constant<int, 64>{});
@@ -1159,6 +1457,31 @@ nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtyp
   });
   if (e != cudaSuccess) return fail(NVFP4_ERR_CUDA, "[%s] %s", tag, cudaGetErrorString(e));
   return check_launch(tag);
+}
+
+nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
+                          const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int64_t B,
+                          int64_t T, int64_t Hq, int64_t max_q, int64_t max_kv, int64_t max_pages, float scale,
+                          int causal, int64_t window, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                          nvfp4_stream_t stream) {
+  return kv_attend("kv_attention", cache, q, q_dt, q_stride, q_start, kv_len, page_table, B, T, Hq, max_q, max_kv,
+                   max_pages, scale, causal, window, nullptr, 0, out, lse, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status kv_attention_tree(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt, int64_t q_stride,
+                               const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                               const uint32_t* tree_mask, int64_t mask_words, int64_t B, int64_t T, int64_t Hq,
+                               int64_t max_q, int64_t max_kv, int64_t max_pages, float scale, int64_t window, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
+  const char* tag = "kv_attention_tree";
+  const int64_t most = max_q < T ? max_q : T;
+  if (mask_words < 0 || mask_words > (1 << 20) || (most > 0 && (mask_words < 1 || (most - 1) / 32 >= mask_words)))
+    return fail(NVFP4_ERR_INVALID_ARG, "[%s] a mask of %lld words does not hold %lld drafts", tag, (long long)mask_words,
+                (long long)most);
+  if (most > 0 && B > 0 && (!tree_mask || !q_start)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null tree_mask or q_start", tag);
+  if (reinterpret_cast<uintptr_t>(tree_mask) & 3u) return fail(NVFP4_ERR_INVALID_ARG, "[%s] tree_mask must be 4-byte aligned", tag);
+  return kv_attend(tag, cache, q, q_dt, q_stride, q_start, kv_len, page_table, B, T, Hq, max_q, max_kv, max_pages, scale, 0,
+                   window, tree_mask, mask_words, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

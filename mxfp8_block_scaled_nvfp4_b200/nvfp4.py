@@ -73,6 +73,15 @@ SIGNATURES = [
     ("gather_qmm_workspace_size", _SZ, [_I64, _I64, _I64]),
     ("gather_qmm_staged_workspace_size", _SZ, [_I64, _I64, _I64, _I64]),
     ("gather_qmm_noalloc", _I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P]),
+    ("rms_norm", _I, [_P, _P, _P, _I, _I64, _I64, ctypes.c_double, _P, _P, _P, _P]),
+    ("rms_norm_quantize", _I, [_I, _P, _P, _P, _I, _I64, _I64, ctypes.c_double, _P, _P, _P, _P, _I, _P, _P]),
+    ("rms_norm_vjp", _I, [_P, _P, _P, _P, _P, _I, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    ("rms_norm_vjp_workspace_size", _SZ, [_I64, _I64]),
+    ("kv_cache_append", _I, [ctypes.POINTER(KvCacheArgs), _P, _P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _I,
+                             _P, _P, _P, _P]),
+    ("kv_cache_move", _I, [ctypes.POINTER(KvCacheArgs), _P, _P, _I64, _P, _I64, _P]),
+    ("kv_attention_tree", _I, [ctypes.POINTER(KvCacheArgs), _P, _I, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                               _I64, ctypes.c_float, _I64, _P, _P, _P, _SZ, _P]),
     ("kv_cache_write", _I, [ctypes.POINTER(KvCacheArgs), _P, _P, _I, _I64, _I64, _I64, _P, _P]),
     ("kv_cache_read", _I, [ctypes.POINTER(KvCacheArgs), _P, _I64, _P, _P, _I, _P]),
     ("kv_attention", _I, [ctypes.POINTER(KvCacheArgs), _P, _I, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
@@ -541,6 +550,115 @@ def gather_qmm_noalloc(x, w_codes, w_scales, g, idx, out=None) -> torch.Tensor:
 
 
 # ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+def _need_norm(x, w, residual, h, rstd):
+    """Types and sizes of a norm's tensors; (rows, K) of x [..., K]."""
+    if x.dtype not in DT:
+        raise ValueError("x must be float32, float16 or bfloat16")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    K = x.shape[-1]
+    rows = x.numel() // K if K else 0
+    _need_dtype(w, x.dtype, "weight")
+    if w.numel() != K:
+        raise ValueError(f"weight must hold {K} elements, got {w.numel()}")
+    for t, what in ((residual, "residual"), (h, "h")):
+        _need_dtype(t, x.dtype, what)
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{what} must be {tuple(x.shape)}, got {tuple(t.shape)}")
+    if h is not None and residual is None:
+        raise ValueError("h is given with a residual, and only then")
+    _need_dtype(rstd, torch.float32, "rstd")
+    _need_bytes(rstd, 4 * rows, "rstd")
+    _need_cuda(x, w, residual, h, rstd)
+    return rows, K
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, h: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+             return_rstd: bool = False):
+    """(y, h): the norm's output y in x's dtype and what was normed, h = x +
+    residual rounded to x's dtype (x itself without a residual), both of x's
+    shape [..., K]; with return_rstd (or an rstd tensor) the triple (y, h,
+    rstd), rstd fp32 [rows] for rms_norm_vjp.  h may be x or residual, to add
+    in place."""
+    rows, K = _need_norm(x, weight, residual, h, rstd)
+    _need_dtype(out, x.dtype, "out")
+    _need_bytes(out, _nbytes(x), "out")
+    _need_cuda(out)
+    out = torch.empty_like(x) if out is None else out
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    if rstd is None and return_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check(lib().rms_norm(_ptr(x), _ptr(residual), _ptr(weight), DT[x.dtype], rows, K, eps, _ptr(h), _ptr(out), _ptr(rstd),
+                          _stream()))
+    y = (out, x if h is None else h)
+    return y if rstd is None else y + (rstd,)
+
+
+def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, mode: str, g: torch.Tensor | None = None, eps: float = 1e-6,
+                      residual: torch.Tensor | None = None, layout: str = "linear", codes: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None, h: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+                      return_rstd: bool = False):
+    """(codes, scales, h): rms_norm's fp32 output quantized as mode's quantizer
+    does (codes int32 [rows, K/8], "mxfp8" K/4; scales uint8 in `layout`; g the
+    fp32 [1] amax of the output, "nvfp4" only), and h as rms_norm gives it; with
+    return_rstd (or an rstd tensor) rstd as well."""
+    if mode not in MODE:
+        raise ValueError("rms_norm_quantize: mode must be nvfp4, mxfp8 or mxfp4")
+    rows, K = _need_norm(x, weight, residual, h, rstd)
+    per, group = 4 if mode == "mxfp8" else 8, 16 if mode == "nvfp4" else 32
+    _need_g(g, 1, "g")
+    _need_bytes(codes, rows * (K // per) * 4, "codes")
+    _need_bytes(scales, _scale_nbytes(rows, K // group, layout), "scales")
+    _need_cuda(g, codes, scales)
+    if codes is None:
+        codes = torch.empty(rows, K // per, dtype=torch.int32, device=x.device)
+    if scales is None:
+        scales = torch.empty(scale_shape(rows, K // group, layout), dtype=torch.uint8, device=x.device)
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    if rstd is None and return_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check(lib().rms_norm_quantize(MODE[mode], _ptr(x), _ptr(residual), _ptr(weight), DT[x.dtype], rows, K, eps, _ptr(g),
+                                   _ptr(h), _ptr(codes), _ptr(scales), LAYOUT[layout], _ptr(rstd), _stream()))
+    y = (codes, scales, x if h is None else h)
+    return y if rstd is None else y + (rstd,)
+
+
+def rms_norm_vjp_workspace_size(rows: int, K: int) -> int:
+    return int(lib().rms_norm_vjp_workspace_size(rows, K))
+
+
+def rms_norm_vjp(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                 dh: torch.Tensor | None = None, dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None):
+    """(dx, dw): gradients of rms_norm and rms_norm_quantize (which passes the
+    gradient of its output straight through).  dy: gradient of the output; h,
+    rstd as the forward call gave them; dh: gradient that reaches h past the
+    norm (None: none).  dx (dy's dtype; it may be dy or dh) is the gradient of
+    x and of residual; dw fp32 [K] that of weight."""
+    rows, K = _need_norm(dy, weight, dh, None, rstd)
+    _need_dtype(h, dy.dtype, "h")
+    if h.shape != dy.shape:
+        raise ValueError(f"h must be {tuple(dy.shape)}, got {tuple(h.shape)}")
+    _need_dtype(dx, dy.dtype, "dx")
+    _need_bytes(dx, _nbytes(dy), "dx")
+    _need_dtype(dw, torch.float32, "dw")
+    _need_bytes(dw, 4 * K, "dw")
+    _need_cuda(h, dx, dw, workspace)
+    dx = torch.empty_like(dy) if dx is None else dx
+    dw = torch.empty(K, dtype=torch.float32, device=dy.device) if dw is None else dw
+    if workspace is None:
+        workspace = torch.empty(rms_norm_vjp_workspace_size(rows, K), dtype=torch.uint8, device=dy.device)
+    _check(lib().rms_norm_vjp(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), DT[dy.dtype], rows, K, _ptr(dx),
+                              _ptr(dw), _ptr(workspace), _nbytes(workspace), _stream()))
+    return dx, dw
+
+
+# ---------------------------------------------------------------------------
 # key/value cache
 # ---------------------------------------------------------------------------
 class KvCache:
@@ -635,6 +753,61 @@ def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torc
                                 slots.data_ptr(), _stream()))
 
 
+def kv_cache_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor,
+                    sin: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, interleaved: bool = False,
+                    q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate the queries q [T, Hq, D] and keys k [T, heads, D] of T new tokens
+    by their positions [T] int32 and quantize keys and values into the cache's
+    slots [T] int32; returns the rotated queries [T, Hq, D] (q's dtype,
+    contiguous).  cos, sin fp32 [max_pos, rot / 2]: the first rot elements of a
+    head turn, in pairs (i, i + rot / 2) or, interleaved, (2i, 2i + 1).  A token
+    with a negative slot is skipped, its row of q_out left as it is."""
+    T, heads, D = slots.shape[0], cache.heads, cache.D
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    Hq = q.shape[1]
+    if q.dtype != k.dtype or k.dtype != v.dtype or k.dtype not in DT:
+        raise ValueError("q, k and v must share a dtype: float32, float16 or bfloat16")
+    _need_dtype(slots, torch.int32, "slots")
+    _need_dtype(positions, torch.int32, "positions")
+    _need_dtype(cos, torch.float32, "cos")
+    _need_dtype(sin, torch.float32, "sin")
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("cos and sin must both be [max_pos, rot / 2]")
+    _need_bytes(positions, 4 * T, "positions")
+    if q_out is not None:
+        _need_dtype(q_out, q.dtype, "q_out")
+        _need_bytes(q_out, T * Hq * D * q.element_size(), "q_out")
+    _need_cuda(slots, positions, cos, sin, q_out)
+    dev = _need_cache(cache)
+    strides = (_need_rows(q, (T, Hq, D), "q", dev), _need_rows(k, (T, heads, D), "k", dev), _need_rows(v, (T, heads, D), "v", dev))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+    _check(lib().kv_cache_append(cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), DT[q.dtype], T, Hq, *strides,
+                                 cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], interleaved,
+                                 positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), _stream()))
+    return q_out
+
+
+def kv_cache_move(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, starts: torch.Tensor | None = None) -> None:
+    """Copy the rows of slots src [M] to slots dst [M] (int32; a negative one
+    skips its move).  starts [S + 1] int32: the moves starts[s] .. starts[s + 1]
+    - 1 of a sequence take effect one after the other; None: every move for
+    itself (no slot is then both written and read or written twice)."""
+    M = src.shape[0]
+    _need_dtype(src, torch.int32, "src")
+    _need_dtype(dst, torch.int32, "dst")
+    _need_dtype(starts, torch.int32, "starts")
+    if dst.shape != src.shape or src.dim() != 1:
+        raise ValueError("src and dst must both be [M]")
+    if starts is not None and (starts.dim() != 1 or starts.shape[0] < 1):
+        raise ValueError("starts must be [S + 1]")
+    _need_cuda(src, dst, starts)
+    _need_cache(cache)
+    _check(lib().kv_cache_move(cache._ref, src.data_ptr(), dst.data_ptr(), M, None if starts is None else starts.data_ptr(),
+                               M if starts is None else starts.shape[0] - 1, _stream()))
+
+
 def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None):
     """(k, v) [T, heads, D]: the values of the slots [T] int32 (negative: zero
     rows)."""
@@ -718,5 +891,64 @@ def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_l
         cache._ref, q.data_ptr(), DT[q.dtype], q_stride, None if q_start is None else q_start.data_ptr(),
         kv_len.data_ptr(), page_table.data_ptr(), B, T, Hq, max_q, max_kv, max_pages,
         cache.D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size, _stream()))
+    return out if lse is None else (out, lse)
+
+
+def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                      tree_mask: torch.Tensor, q_start: torch.Tensor, max_q: int | None = None, max_kv: int | None = None,
+                      scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, return_lse: bool = False, workspace: torch.Tensor | None = None):
+    """kv_attention for drafted tokens that form trees: the queries q
+    [q_start[b] .. q_start[b + 1]) are the last of sequence b's kv_len[b] cached
+    tokens, and each sees the context before them and of them those in its row
+    of tree_mask [T, words] int32 (bit d % 32 of word d / 32: draft d, itself
+    included only where its bit is set; 32 * words >= max_q).  window: the
+    context within window tokens of the query's place in its branch (the number
+    of drafts it sees, less one).  The rest as in kv_attention."""
+    T, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    # (what is None is not looked at: a decoding call is short)
+    if page_table.dtype != torch.int32 or kv_len.dtype != torch.int32 or kv_len.numel() < B:
+        _need_dtype(page_table, torch.int32, "page_table")
+        _need_dtype(kv_len, torch.int32, "kv_len")
+        _need_bytes(kv_len, 4 * B, "kv_len")
+    _need_dtype(q_start, torch.int32, "q_start")
+    _need_bytes(q_start, 4 * (B + 1), "q_start")
+    if tree_mask.dtype != torch.int32 and tree_mask.dtype != torch.uint32:
+        raise ValueError(f"tree_mask must be {torch.int32}, got {tree_mask.dtype}")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError(f"tree_mask must be [{T}, words], got {tuple(tree_mask.shape)}")
+    _need_cuda(page_table, kv_len, q_start, tree_mask)
+    if out is not None:
+        _need_dtype(out, q.dtype, "out")
+        _need_bytes(out, T * Hq * D * q.element_size(), "out")
+        _need_cuda(out)
+    if lse is not None:
+        _need_dtype(lse, torch.float32, "lse")
+        _need_bytes(lse, 4 * T * Hq, "lse")
+        _need_cuda(lse)
+    if workspace is not None:
+        _need_cuda(workspace)
+    q_stride = _need_rows(q, (T, Hq, cache.D), "q", _need_cache(cache))
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
+    if max_q is None:
+        max_q = T
+    if max_kv is None:
+        max_kv = max_pages * cache.page_size
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+    if lse is None and return_lse:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        size = kv_attention_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
+        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device) if size else None
+    else:
+        size = _nbytes(workspace)
+    _check(lib().kv_attention_tree(
+        cache._ref, q.data_ptr(), DT[q.dtype], q_stride, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+        tree_mask.data_ptr(), tree_mask.shape[1], B, T, Hq, max_q, max_kv, max_pages,
+        cache.D ** -0.5 if scale is None else scale, window, out.data_ptr(),
         None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size, _stream()))
     return out if lse is None else (out, lse)
