@@ -27,11 +27,18 @@ struct AppendArgs {
   const int32_t* positions;
   uint32_t max_pos, rot;
   int interleaved;
-  uint32_t q_units, q_ctas, kv_ctas;  // 16-element units; CTAs of Q, of K and of V
-  FastDiv q_per_token;      // Hq * D / 16
+  uint32_t Hq, q_groups;    // groups of heads that one thread takes
+  uint32_t q_units, q_ctas, kv_ctas;  // threads of Q; CTAs of Q, of K and of V
+  FastDiv q_per_token;      // q_groups * D / 16
 };
 
-// Elements 8 i .. 8 i + 8 of a head, rotated.
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+  x = u;
+}
+
+// Elements e .. e + 8 of a head, rotated.
 template <typename T>
 __device__ __forceinline__ void turn8(const AppendArgs& a, const T* head, uint32_t pos, uint32_t e, float* v) {
   if (e >= a.rot) return;
@@ -42,11 +49,7 @@ __device__ __forceinline__ void turn8(const AppendArgs& a, const T* head, uint32
     const float4 c = __ldg(reinterpret_cast<const float4*>(cr + e / 2u)), s = __ldg(reinterpret_cast<const float4*>(sr + e / 2u));
     const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = v[2 * i], y = v[2 * i + 1];
-      v[2 * i] = __fsub_rn(__fmul_rn(x, cc[i]), __fmul_rn(y, ss[i]));
-      v[2 * i + 1] = __fadd_rn(__fmul_rn(y, cc[i]), __fmul_rn(x, ss[i]));
-    }
+    for (int i = 0; i < 4; ++i) turn(v[2 * i], v[2 * i + 1], cc[i], ss[i]);
     return;
   }
   const bool low = e < half;
@@ -62,22 +65,82 @@ __device__ __forceinline__ void turn8(const AppendArgs& a, const T* head, uint32
   }
 }
 
-// One thread per 16 elements; CTAs of Q first, then of K, then of V.
-template <typename T, int MODE, bool V8>
-__global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
-  const bool is_q = blockIdx.x < a.q_ctas;
-  const uint32_t side = is_q ? 0u : (blockIdx.x - a.q_ctas) / a.kv_ctas;
-  const uint32_t u = (is_q ? blockIdx.x : blockIdx.x - a.q_ctas - side * a.kv_ctas) * kRowThreads + threadIdx.x;
-  const bool in = u < (is_q ? a.q_units : a.r.units);
-  Unit w;
-  {
-    const FastDiv& pt = is_q ? a.q_per_token : a.r.per_token;
-    const uint32_t x = in ? u : 0u;
-    w.t = pt.div(x);
-    const uint32_t y = x - w.t * pt.d;
-    w.h = a.r.per_head.div(y);
-    w.j = y - w.h * a.r.per_head.d;
+// A thread's 16 elements of a query head: eight and their partners, so that
+// nothing is loaded twice; HEADS heads of a token, which share the angles.
+template <typename T, int HEADS>
+__device__ __forceinline__ void turn_queries(const AppendArgs& a, uint32_t u) {
+  if (u >= a.q_units) return;
+  const uint32_t t = a.q_per_token.div(u), y = u - t * a.q_per_token.d;
+  const uint32_t grp = a.r.per_head.div(y), j = y - grp * a.r.per_head.d;
+  const int32_t slot = __ldg(a.r.slots + t), pos = __ldg(a.positions + t);
+  if (slot < 0) return;
+  if ((uint32_t)slot >= a.r.num_slots || (uint32_t)pos >= a.max_pos) {
+    atomicOr(&g_device_error, (unsigned)kDevErrIndex);
+    return;
   }
+  const uint32_t half = a.rot / 2u, D = a.r.D, h0 = grp * HEADS;
+  const bool turns = j * 16u < a.rot, pairs = turns && !a.interleaved;
+  const uint32_t e0 = pairs ? j * 8u : j * 16u, e1 = pairs ? e0 + half : e0 + 8u;
+  const T* q = static_cast<const T*>(a.q) + (int64_t)t * a.q_stride + (int64_t)h0 * D;
+  T* out = static_cast<T*>(a.q_out) + ((int64_t)t * a.Hq + h0) * D;
+  constexpr int W = sizeof(T) == 4 ? 2 : 1;
+  uint4 x[HEADS][2][W];
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h)
+    if (h0 + h < a.Hq)
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        x[h][0][w] = __ldg(reinterpret_cast<const uint4*>(q + h * D + e0) + w);
+        x[h][1][w] = __ldg(reinterpret_cast<const uint4*>(q + h * D + e1) + w);
+      }
+  float c[8], s[8];
+  if (turns) {
+    load8<float>(a.cs[0] + (uint64_t)pos * half + j * 8u, c);
+    load8<float>(a.cs[1] + (uint64_t)pos * half + j * 8u, s);
+  }
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    if (h0 + h >= a.Hq) return;
+    float v[16];
+    {
+      float lo[8], hi[8];
+      unpack8<T>(x[h][0][0], x[h][0][W - 1], lo);
+      unpack8<T>(x[h][1][0], x[h][1][W - 1], hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = lo[i];
+        v[8 + i] = hi[i];
+      }
+    }
+    if (pairs) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn(v[i], v[8 + i], c[i], s[i]);
+    } else if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn(v[2 * i], v[2 * i + 1], c[i], s[i]);
+    }
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = v[i];
+      hi[i] = v[8 + i];
+    }
+    store8<T>(out + h * D + e0, lo);
+    store8<T>(out + h * D + e1, hi);
+  }
+}
+
+// CTAs of Q first, then of K, then of V; of these a thread has 16 elements.
+template <typename T, int MODE, bool V8, int HEADS>
+__global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
+  if (blockIdx.x < a.q_ctas) {
+    turn_queries<T, HEADS>(a, blockIdx.x * kRowThreads + threadIdx.x);
+    return;
+  }
+  const uint32_t side = blockIdx.x - a.q_ctas >= a.kv_ctas ? 1u : 0u;
+  const uint32_t u = (blockIdx.x - a.q_ctas - side * a.kv_ctas) * kRowThreads + threadIdx.x;
+  const bool in = u < a.r.units;
+  const Unit w = unit_at(a.r, in ? u : 0u);
   const int32_t slot = in ? __ldg(a.r.slots + w.t) : -1;
   const int32_t pos = in ? __ldg(a.positions + w.t) : 0;
   const bool bad = slot >= 0 && ((uint32_t)slot >= a.r.num_slots || (uint32_t)pos >= a.max_pos);
@@ -87,7 +150,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = 0.0f;
   if (go) {
-    const T* head = static_cast<const T*>(is_q ? a.q : a.r.x[side]) + (int64_t)w.t * (is_q ? a.q_stride : a.r.stride[side]) + (int64_t)w.h * a.r.D;
+    const T* head = static_cast<const T*>(a.r.x[side]) + (int64_t)w.t * a.r.stride[side] + (int64_t)w.h * a.r.D;
     RawBlk<T> raw;
     load_blk<T, V8>(head + w.j * 16u, raw);
     unpack16<T>(raw, v);
@@ -95,13 +158,6 @@ __global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant
       turn8<T>(a, head, (uint32_t)pos, w.j * 16u, v);
       turn8<T>(a, head, (uint32_t)pos, w.j * 16u + 8u, v + 8);
     }
-  }
-  if (is_q) {
-    if (!go) return;
-    RawBlk<T> out;
-    norm::pack16<T>(v, out);
-    norm::store_blk<T, V8>(static_cast<T*>(a.q_out) + (int64_t)u * 16, out);
-    return;
   }
   const float E = MODE == kNV && a.r.g[side] ? kGlobalEncode / __ldg(a.r.g[side]) : 1.0f;
   uint4 q;
@@ -116,11 +172,12 @@ __global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// Moves: the moves of a sequence take effect one after the other.  A thread
-// has one piece (at most 16 bytes of one head's codes or scales) of all rows
-// that a sequence moves, so that no two threads touch the same bytes; it reads
-// the pieces of kMoves moves before it writes them, and takes a piece that an
-// earlier one of them writes from there.
+// Moves.  A thread has one piece (at most 16 bytes of one head's codes or
+// scales) of the keys' rows and the same of the values', of one move, or, where
+// the moves of a sequence take effect one after the other, of all of them: no
+// two threads then touch the same bytes.  Such a thread reads the pieces of
+// kMoves moves before it writes them, and takes a piece that an earlier one of
+// them writes from there.
 // ---------------------------------------------------------------------------
 constexpr int kMoves = 8;
 
@@ -133,7 +190,7 @@ struct MoveArgs {
   uint32_t M, S, heads, page_size, num_slots;
   uint32_t row[2];          // bytes of a row's codes, of its scales
   uint32_t piece;           // bytes of a scale piece: 1, 2, 4, 8 or 16
-  uint32_t code_pieces, pieces;  // of a row and side; of a row
+  uint32_t code_pieces, pieces;  // of a side's row: of its codes; all
   uint32_t units;           // S * heads * pieces
   FastDiv per_seq, per_head, by_page;
 };
@@ -159,52 +216,73 @@ __device__ __forceinline__ void store_piece(uint8_t* p, uint32_t bytes, const ui
   else *p = (uint8_t)v.x;
 }
 
+template <bool ORDERED>
 __global__ void __launch_bounds__(kRowThreads) k_kv_move(const __grid_constant__ MoveArgs a) {
   const uint32_t u = blockIdx.x * kRowThreads + threadIdx.x;
   if (u >= a.units) return;
   const uint32_t s = a.per_seq.div(u), y = u - s * a.per_seq.d, h = a.per_head.div(y), p = y - h * a.per_head.d;
-  int64_t m0 = s, m1 = (int64_t)s + 1;
-  if (a.starts) {
-    m0 = __ldg(a.starts + s);
-    m1 = __ldg(a.starts + s + 1);
-    if (m0 < 0 || m1 < m0 || m1 > (int64_t)a.M) {
-      atomicOr(&g_device_error, (unsigned)kDevErrIndex);
-      return;
-    }
-  }
-  const bool codes = p < 2u * a.code_pieces;
-  const uint32_t of_side = codes ? a.code_pieces : a.pieces / 2u - a.code_pieces, i = codes ? p : p - 2u * a.code_pieces;
-  const uint32_t side = i >= of_side ? 1u : 0u, bytes = codes ? 16u : a.piece, row_bytes = a.row[codes ? 0 : 1];
-  uint8_t* base = (codes ? a.codes[side] : a.scales[side]) + (uint64_t)(i - side * of_side) * bytes;
+  const bool codes = p < a.code_pieces;
+  const uint32_t bytes = codes ? 16u : a.piece, row_bytes = a.row[codes ? 0 : 1];
+  const uint32_t first = (codes ? p : p - a.code_pieces) * bytes;
+  uint8_t* k = (codes ? a.codes[0] : a.scales[0]) + first;
+  uint8_t* v = (codes ? a.codes[1] : a.scales[1]) + first;
   auto at = [&](int32_t slot) {
     const uint32_t page = a.by_page.div((uint32_t)slot);
-    return base + (((uint64_t)page * a.heads + h) * a.page_size + ((uint32_t)slot - page * a.page_size)) * row_bytes;
+    return (((uint64_t)page * a.heads + h) * a.page_size + ((uint32_t)slot - page * a.page_size)) * row_bytes;
   };
+  // whether move m is made
+  auto named = [&](int32_t from, int32_t to) {
+    if (from < 0 || to < 0) return false;
+    if ((uint32_t)from < a.num_slots && (uint32_t)to < a.num_slots) return true;
+    atomicOr(&g_device_error, (unsigned)kDevErrIndex);
+    return false;
+  };
+  if constexpr (!ORDERED) {
+    const int32_t from = __ldg(a.src + s), to = __ldg(a.dst + s);
+    if (!named(from, to)) return;
+    const uint64_t x = at(from), z = at(to);
+    const uint4 pk = load_piece(k + x, bytes), pv = load_piece(v + x, bytes);
+    store_piece(k + z, bytes, pk);
+    store_piece(v + z, bytes, pv);
+    return;
+  }
+  const int64_t m0 = __ldg(a.starts + s), m1 = __ldg(a.starts + s + 1);
+  if (m0 < 0 || m1 < m0 || m1 > (int64_t)a.M) {
+    atomicOr(&g_device_error, (unsigned)kDevErrIndex);
+    return;
+  }
   for (int64_t m = m0; m < m1; m += kMoves) {
     int32_t from[kMoves], to[kMoves];
-    uint4 v[kMoves];
+    uint4 pk[kMoves], pv[kMoves];
 #pragma unroll
-    for (int k = 0; k < kMoves; ++k) {
-      from[k] = m + k < m1 ? __ldg(a.src + m + k) : -1;
-      to[k] = m + k < m1 ? __ldg(a.dst + m + k) : -1;
-      const bool named = from[k] >= 0 && to[k] >= 0;
-      if (named && ((uint32_t)from[k] >= a.num_slots || (uint32_t)to[k] >= a.num_slots)) {
-        atomicOr(&g_device_error, (unsigned)kDevErrIndex);
-        from[k] = to[k] = -1;
-      }
-      if (!named) from[k] = to[k] = -1;
+    for (int i = 0; i < kMoves; ++i) {
+      from[i] = m + i < m1 ? __ldg(a.src + m + i) : -1;
+      to[i] = m + i < m1 ? __ldg(a.dst + m + i) : -1;
     }
 #pragma unroll
-    for (int k = 0; k < kMoves; ++k)
-      if (from[k] >= 0) v[k] = load_piece(at(from[k]), bytes);
+    for (int i = 0; i < kMoves; ++i) {
+      if (!named(from[i], to[i])) from[i] = to[i] = -1;
+      if (from[i] >= 0) {
+        const uint64_t x = at(from[i]);
+        pk[i] = load_piece(k + x, bytes);
+        pv[i] = load_piece(v + x, bytes);
+      }
+    }
 #pragma unroll
-    for (int k = 1; k < kMoves; ++k)
+    for (int i = 1; i < kMoves; ++i)
 #pragma unroll
-      for (int e = 0; e < k; ++e)  // the last of the earlier writes counts
-        if (to[e] >= 0 && to[e] == from[k]) v[k] = v[e];
+      for (int e = 0; e < i; ++e)  // the last of the earlier writes counts
+        if (to[e] >= 0 && to[e] == from[i]) {
+          pk[i] = pk[e];
+          pv[i] = pv[e];
+        }
 #pragma unroll
-    for (int k = 0; k < kMoves; ++k)
-      if (from[k] >= 0) store_piece(at(to[k]), bytes, v[k]);
+    for (int i = 0; i < kMoves; ++i)
+      if (from[i] >= 0) {
+        const uint64_t z = at(to[i]);
+        store_piece(k + z, bytes, pk[i]);
+        store_piece(v + z, bytes, pv[i]);
+      }
   }
 }
 

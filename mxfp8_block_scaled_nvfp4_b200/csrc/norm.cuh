@@ -54,7 +54,7 @@ struct VjpArgs {
   float* part;           // [parts, K]
   uint32_t parts;
   int64_t rows;
-  uint32_t K, blocks, row_warps;
+  uint32_t K, row_warps;
 };
 
 // A block of 16 elements.  Plain loads, not the read-only path: h may take x's
@@ -120,11 +120,13 @@ __device__ __forceinline__ F row_sum(F v, F* red, uint32_t row_warps, uint32_t f
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (row_warps == 1) return v;
-  if ((threadIdx.x & 31u) == 0) red[threadIdx.x >> 5] = v;
+  const uint32_t lane = threadIdx.x & 31u;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[first];
-  for (uint32_t i = 1; i < row_warps; ++i) v += red[first + i];
-  return v;
+  v = lane < row_warps ? red[first + lane] : F(0);  // at most 16 warps
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // Codes and scale byte of this lane's 16 fp32 values (MX: of the lane pair's
@@ -275,103 +277,145 @@ __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant_
   if constexpr (OUT != kPlain) zero_scale_padding(a.so, (uint32_t)a.rows);
 }
 
-// The parts of dw stay in registers over all rows of a CTA; dy and h do over a
-// row where they fit beside them (HOLD), and are read twice elsewhere.
-template <typename T, int U>
+// The part of dw that a CTA's rows make stays in registers.  A thread has N
+// 16-byte pieces of a row, a row's threads' pieces side by side.  STAGED (N
+// pieces of 16 elements, K <= 8192): rows are copied into shared memory one or
+// two ahead, each thread's pieces into slots of its own, so that no barrier
+// stands between copy and use; longer rows are read twice.
+template <typename T>
+constexpr int kVjpStages = sizeof(T) == 4 ? 2 : 3;
+template <typename T>
+constexpr uint32_t kVjpSmem = kVjpStages<T> * 3 * 16 * sizeof(T);  // bytes a thread
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// A 16-byte piece as fp32.
+template <typename T>
+__device__ __forceinline__ void piece_to_f(const uint4& p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = __uint_as_float(p.x);
+    v[1] = __uint_as_float(p.y);
+    v[2] = __uint_as_float(p.z);
+    v[3] = __uint_as_float(p.w);
+  } else {
+    float x[8];
+    unpack8<T>(p, p, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 piece_of_f(const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  } else {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = std::is_same<T, __half>::value ? pack_f16x2(v[2 * i], v[2 * i + 1]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    return make_uint4(p[0], p[1], p[2], p[3]);
+  }
+}
+
+template <typename T, bool STAGED>
 __global__ void __launch_bounds__(kMaxThreads) k_rms_norm_vjp(const __grid_constant__ VjpArgs a) {
-  constexpr bool HOLD = U == 1, V8 = U == 1;
+  constexpr int E = 16 / (int)sizeof(T), N = (STAGED ? 16 : 64) / E, ST = kVjpStages<T>;
+  extern __shared__ __align__(16) uint4 slots[];  // [stage][dy, h, dh][piece][thread]
   __shared__ float red[2][kMaxThreads / 32];
   const uint32_t warp = threadIdx.x >> 5, rpc = (blockDim.x >> 5) / a.row_warps;
   const uint32_t mine = warp / a.row_warps, first = mine * a.row_warps, span = a.row_warps * 32u;
-  const uint32_t b0 = threadIdx.x - first * 32u;
-  const T* w = static_cast<const T*>(a.w);
-  constexpr int N = HOLD ? U : 1;
-  RawBlk<T> dy[N], h[N], wr[N], dh;
-  float acc[U][16];
-  auto load_w = [&](int u) {
-    const uint32_t b = b0 + span * u;
-    if (b < a.blocks) load_blk<T, V8>(w + b * 16u, wr[u % N]);
-    else zero(wr[u % N]);
-  };
-  auto load = [&](int64_t row, int u) {
-    const uint32_t b = b0 + span * u;
-    if (row < a.rows && b < a.blocks) {
-      const int64_t at = row * a.K + (int64_t)b * 16;
-      load_rw<T, V8>(static_cast<const T*>(a.dy) + at, dy[u % N]);
-      load_rw<T, V8>(static_cast<const T*>(a.h) + at, h[u % N]);
-    } else {
-      zero(dy[u % N]);
-      zero(h[u % N]);
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if constexpr (HOLD) load_w(u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
-  }
+  const uint32_t p0 = threadIdx.x - first * 32u, pieces = a.K / E;  // this thread's pieces: p0 + span n
+  const uint4* src[3] = {static_cast<const uint4*>(a.dy), static_cast<const uint4*>(a.h), static_cast<const uint4*>(a.dh)};
+  const uint4* w = static_cast<const uint4*>(a.w);
+  const uint4 none = make_uint4(0, 0, 0, 0);
   const int64_t step = (int64_t)gridDim.x * rpc;
   int64_t row = (int64_t)blockIdx.x * rpc + mine;
-  uint32_t turn = 0;
+  uint4 wr[STAGED ? N : 1];
+  float acc[N][E];
+  // Piece n of tensor t in a row: plain loads, dx may take dy's or dh's place.
+  auto load = [&](int64_t row, int t, int n) {
+    uint4 v = none;
+    const uint32_t p = p0 + span * n;
+    if (row < a.rows && p < pieces && (t < 2 || a.dh))
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src[t] + row * pieces + p));
+    return v;
+  };
+  auto slot = [&](uint32_t st, int t, int n) { return slots + ((st * 3 + t) * N + n) * blockDim.x + threadIdx.x; };
+  auto start = [&](int64_t row, uint32_t st) {
+    if (row < a.rows)
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        if (t < 2 || a.dh)
+#pragma unroll
+          for (int n = 0; n < N; ++n)
+            if (p0 + span * n < pieces)
+              copy_async16((uint32_t)__cvta_generic_to_shared(slot(st, t, n)), src[t] + row * pieces + (p0 + span * n));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint32_t turn = 0, st = 0;
+  auto get = [&](int t, int n) -> uint4 {
+    if constexpr (STAGED) return row < a.rows && p0 + span * n < pieces && (t < 2 || a.dh) ? *slot(st, t, n) : none;
+    else return load(row, t, n);
+  };
+  auto weight = [&](int n) -> uint4 {
+    if constexpr (STAGED) return wr[n];
+    else return p0 + span * n < pieces ? __ldg(w + (p0 + span * n)) : none;
+  };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int i = 0; i + 1 < ST; ++i) start(row + i * step, i);
+#pragma unroll
+    for (int n = 0; n < N; ++n) wr[n] = p0 + span * n < pieces ? __ldg(w + (p0 + span * n)) : none;
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[n][i] = 0.0f;
+  const float per_k = 1.0f / (float)a.K;
   for (int64_t base = (int64_t)blockIdx.x * rpc; base < a.rows; base += step, row += step, turn ^= 1u) {
     const float r = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
-    float s = 0.0f;
-    if constexpr (HOLD) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) load(row, u);
+    if constexpr (STAGED) {
+      start(row + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
     }
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if constexpr (!HOLD) {
-        load(row, u);
-        load_w(u);
-      }
-      float d[16], x[16], c[16];
-      unpack16<T>(dy[u % N], d);
-      unpack16<T>(h[u % N], x);
-      unpack16<T>(wr[u % N], c);
+    for (int n = 0; n < N; ++n) {
+      float d[E], x[E], c[E];
+      piece_to_f<T>(get(0, n), d);
+      piece_to_f<T>(get(1, n), x);
+      piece_to_f<T>(weight(n), c);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s = fmaf(d[i] * c[i], x[i], s);
-        acc[u][i] = fmaf(d[i], x[i] * r, acc[u][i]);
+      for (int i = 0; i < E; ++i) {
+        part[i & 3] = fmaf(d[i] * c[i], x[i], part[i & 3]);
+        acc[n][i] = fmaf(d[i], x[i] * r, acc[n][i]);
       }
     }
-    s = row_sum(s, red[turn], a.row_warps, first);
-    const float f = s / (float)a.K * r * r;
+    const float s = row_sum((part[0] + part[1]) + (part[2] + part[3]), red[turn], a.row_warps, first);
+    const float f = s * per_k * r * r;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t b = b0 + span * u;
-      const bool in = row < a.rows && b < a.blocks;
-      if constexpr (!HOLD) {
-        load(row, u);
-        load_w(u);
-      }
-      const int64_t at = row * a.K + (int64_t)b * 16;
-      if (a.dh && in) load_rw<T, V8>(static_cast<const T*>(a.dh) + at, dh);
-      else zero(dh);
-      float d[16], x[16], c[16];
-      unpack16<T>(dy[u % N], d);
-      unpack16<T>(h[u % N], x);
-      unpack16<T>(wr[u % N], c);
+    for (int n = 0; n < N; ++n) {
+      float d[E], x[E], c[E], g[E];
+      piece_to_f<T>(get(0, n), d);
+      piece_to_f<T>(get(1, n), x);
+      piece_to_f<T>(weight(n), c);
+      piece_to_f<T>(get(2, n), g);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fmaf(-x[i], f, d[i] * c[i]);
-      unpack16<T>(dh, c);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], r, c[i]);
-      RawBlk<T> y;
-      pack16<T>(x, y);
-      if (in) store_blk<T, V8>(static_cast<T*>(a.dx) + at, y);
+      for (int i = 0; i < E; ++i) x[i] = fmaf(fmaf(-x[i], f, d[i] * c[i]), r, g[i]);
+      if (row < a.rows && p0 + span * n < pieces) static_cast<uint4*>(a.dx)[row * pieces + (p0 + span * n)] = piece_of_f<T>(x);
     }
+    st = st + 1 == ST ? 0 : st + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!a.dw) return;
   float* part = a.part + ((uint64_t)blockIdx.x * rpc + mine) * a.K;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint32_t b = b0 + span * u;
-    if (b >= a.blocks) continue;
+  for (int n = 0; n < N; ++n) {
+    if (p0 + span * n >= pieces) continue;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<float4*>(part + b * 16u + i) = make_float4(acc[u][i], acc[u][i + 1], acc[u][i + 2], acc[u][i + 3]);
+    for (int i = 0; i < E; i += 4)
+      *reinterpret_cast<float4*>(part + (p0 + span * n) * E + i) = make_float4(acc[n][i], acc[n][i + 1], acc[n][i + 2], acc[n][i + 3]);
   }
 }
 
@@ -380,6 +424,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rms_norm_vjp(const __grid_const
 __global__ void __launch_bounds__(256) k_rms_norm_dw(const __grid_constant__ VjpArgs a) {
   __shared__ float4 sum[32][8];
   const uint32_t c = threadIdx.x & 7u, grp = threadIdx.x >> 3, col = blockIdx.x * 32u + c * 4u;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < a.K)
 #pragma unroll 4

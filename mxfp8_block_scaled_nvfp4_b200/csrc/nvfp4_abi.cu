@@ -927,21 +927,15 @@ nvfp4_status rms_norm_quantize(nvfp4_mode mode, const void* x, const void* resid
 
 // CTAs of k_rms_norm_vjp, and parts of dw (one for each row that a CTA takes
 // at a time).
-constexpr int64_t kNormVjpCtas = 148 * 2;
 static int64_t norm_vjp_ctas(const NormPlan& p, int64_t rows) {
-  const int64_t rpc = p.warps / p.row_warps, want = (rows + rpc - 1) / rpc;
-  return want < kNormVjpCtas ? want : kNormVjpCtas;
+  const int64_t rpc = p.warps / p.row_warps, want = (rows + rpc - 1) / rpc, most = p.warps > 8 ? 148 : 148 * 2;
+  return want < most ? want : most;
 }
 
 size_t rms_norm_vjp_workspace_size(int64_t rows, int64_t K) {
   if (rows < 1 || K < 16 || K % 16 != 0 || K > kNormMaxK || product_exceeds(rows, K, kMaxElems)) return 0;
-  size_t most = 0;
-  for (int v8 = 0; v8 < 2; ++v8) {
-    const NormPlan p = norm_plan(K / 16, v8 != 0);
-    const size_t bytes = (size_t)norm_vjp_ctas(p, rows) * (p.warps / p.row_warps) * (size_t)K * 4;
-    if (bytes > most) most = bytes;
-  }
-  return most;
+  const NormPlan p = norm_plan(K / 16, true);
+  return (size_t)norm_vjp_ctas(p, rows) * (p.warps / p.row_warps) * (size_t)K * 4;
 }
 
 nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
@@ -973,21 +967,37 @@ nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const fl
   a.part = static_cast<float*>(workspace);
   a.rows = rows;
   a.K = (uint32_t)K;
-  a.blocks = (uint32_t)(K / 16);
+  cudaError_t e = cudaSuccess;
   if (rows > 0) {
-    const bool v8 = aligned32(dy) && aligned32(h) && aligned32(w) && aligned32(dh) && aligned32(dx) && K * dt_size(dt) % 32 == 0;
-    const NormPlan p = norm_plan(a.blocks, v8);
+    const NormPlan p = norm_plan(K / 16, true);
     a.row_warps = p.row_warps;
     const int64_t ctas = norm_vjp_ctas(p, rows);
     a.parts = (uint32_t)(ctas * (p.warps / p.row_warps));
     dispatch_dt(dt, [&](auto tag_t) {
       using T = decltype(tag_t);
-      dispatch_norm(p, [&](auto u) {
-        norm::k_rms_norm_vjp<T, decltype(u)::value><<<(unsigned)ctas, p.warps * 32u, 0, stream>>>(a);
-      });
+      if (!p.one) {
+        norm::k_rms_norm_vjp<T, false><<<(unsigned)ctas, p.warps * 32u, 0, stream>>>(a);
+        return;
+      }
+      auto kern = norm::k_rms_norm_vjp<T, true>;
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(norm::kMaxThreads * norm::kVjpSmem<T>));
+      if (e == cudaSuccess) kern<<<(unsigned)ctas, p.warps * 32u, p.warps * 32u * norm::kVjpSmem<T>, stream>>>(a);
     });
   }
-  if (dw) norm::k_rms_norm_dw<<<(unsigned)((K + 31) / 32), 256, 0, stream>>>(a);
+  if (dw && e == cudaSuccess) {  // its launch overlaps the kernel before it
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)((K + 31) / 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = rows > 0 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, norm::k_rms_norm_dw, a);
+  }
+  if (e != cudaSuccess) return fail(NVFP4_ERR_CUDA, "[%s] %s", tag, cudaGetErrorString(e));
   return check_launch(tag);
 }
 
@@ -1158,19 +1168,23 @@ nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* q, const v
   a.max_pos = (uint32_t)max_pos;
   a.rot = (uint32_t)rot;
   a.interleaved = interleaved != 0;
-  a.q_units = (uint32_t)(T * q_width / 16);
-  a.q_per_token.init((uint32_t)(q_width / 16));
+  a.Hq = (uint32_t)Hq;
+  // four heads a thread where that still fills the GPU
+  const bool few = T * q_width / 16 < 4 * 148 * 2048;
+  a.q_groups = few ? a.Hq : (a.Hq + 3) / 4;
+  a.q_units = (uint32_t)(T * a.q_groups * (cache->D / 16));
+  a.q_per_token.init((uint32_t)(a.q_groups * (cache->D / 16)));
   a.q_ctas = (a.q_units + kv::kRowThreads - 1) / kv::kRowThreads;
   a.kv_ctas = (a.r.units + kv::kRowThreads - 1) / kv::kRowThreads;
-  const bool v8 = rows_aligned32(q, T, q_stride, dt) && rows_aligned32(k, T, k_stride, dt) && rows_aligned32(v, T, v_stride, dt) &&
-                  aligned32(q_out);
+  const bool v8 = rows_aligned32(k, T, k_stride, dt) && rows_aligned32(v, T, v_stride, dt);
   dispatch_dt(dt, [&](auto tag_t) {
     using E = decltype(tag_t);
     dispatch_mode(cache->mode, [&](auto m) {
       constexpr int MODE = decltype(m)::value;
       const unsigned grid = a.q_ctas + 2u * a.kv_ctas;
-      if (v8) kv::k_kv_append<E, MODE, true><<<grid, kv::kRowThreads, 0, stream>>>(a);
-      else kv::k_kv_append<E, MODE, false><<<grid, kv::kRowThreads, 0, stream>>>(a);
+      auto go = [&](auto kern) { kern<<<grid, kv::kRowThreads, 0, stream>>>(a); };
+      if (few) v8 ? go(kv::k_kv_append<E, MODE, true, 1>) : go(kv::k_kv_append<E, MODE, false, 1>);
+      else v8 ? go(kv::k_kv_append<E, MODE, true, 4>) : go(kv::k_kv_append<E, MODE, false, 4>);
     });
   });
   return check_launch(tag);
@@ -1186,9 +1200,9 @@ nvfp4_status kv_cache_move(const nvfp4_kv_cache* cache, const int32_t* src, cons
   const int64_t blocks = cache->D / (cache->mode == NVFP4_MODE_NVFP4 ? 16 : 32);
   const int64_t code_bytes = cache->D / (cache->mode == NVFP4_MODE_MXFP8 ? 1 : 2);
   const int64_t piece = blocks & -blocks;  // the largest power of two that divides a row's scale bytes: 1 to 16
-  const int64_t pieces = 2 * (code_bytes / 16 + blocks / piece);
-  if (product_exceeds(S, cache->heads * pieces, INT32_MAX))
-    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] S*heads*%lld must be below 2^31", tag, (long long)pieces);
+  const int64_t pieces = code_bytes / 16 + blocks / piece;
+  if (product_exceeds(S, cache->heads * 2 * pieces, INT32_MAX))
+    return fail(NVFP4_ERR_UNSUPPORTED, "[%s] S*heads*%lld must be below 2^31", tag, (long long)(2 * pieces));
   if (M > 0 && (!src || !dst)) return fail(NVFP4_ERR_INVALID_ARG, "[%s] null pointer", tag);
   if ((reinterpret_cast<uintptr_t>(src) & 3u) || (reinterpret_cast<uintptr_t>(dst) & 3u) || (reinterpret_cast<uintptr_t>(starts) & 3u))
     return fail(NVFP4_ERR_INVALID_ARG, "[%s] src, dst and starts must be 4-byte aligned", tag);
@@ -1219,7 +1233,9 @@ nvfp4_status kv_cache_move(const nvfp4_kv_cache* cache, const int32_t* src, cons
   a.per_seq.init((uint32_t)(cache->heads * pieces));
   a.per_head.init((uint32_t)pieces);
   a.by_page.init(a.page_size);
-  kv::k_kv_move<<<(a.units + kv::kRowThreads - 1) / kv::kRowThreads, kv::kRowThreads, 0, stream>>>(a);
+  const unsigned grid = (a.units + kv::kRowThreads - 1) / kv::kRowThreads;
+  if (starts) kv::k_kv_move<true><<<grid, kv::kRowThreads, 0, stream>>>(a);
+  else kv::k_kv_move<false><<<grid, kv::kRowThreads, 0, stream>>>(a);
   return check_launch(tag);
 }
 
