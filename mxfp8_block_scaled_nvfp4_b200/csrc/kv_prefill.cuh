@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[2][2], empty[2][2], s_full[2], p_full[2], o_done[2], all_done;  // full, empty: [side][stage]
   __shared__ float other[NQ][2][128];  // maxima (later sums) that the two threads of a row exchange
+  __shared__ float row_factor[NQ][128];  // logit (log2 units) of an accumulator
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_flag;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -329,45 +330,93 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // The producers' first copies: what a copy waits for (lengths, page table) is
+  // long beside them, and so are the queries' way into shared memory below.
+  using W = Raw<MODE, DP>;
+  const uint32_t p = threadIdx.x, tok = p % NT, e0 = p / NT * S::EPT;
+  // tile n's token: its page number is loaded a tile before its row is
+  // wanted, its codes and scales a tile before they are decoded
+  int32_t page = -1;
+  auto page_of = [&](int32_t n) {
+    const int32_t j = begin + n * NT + (int32_t)tok;
+    page = n < iters && j >= rg.lo && j < end ? __ldg(table + a.by_page.div((uint32_t)j)) : -1;
+  };
+  uint64_t src_row = 0;
+  bool there = false;
+  auto fetch = [&](int32_t q) {  // tile q / 2, side q % 2
+    const int32_t n = q >> 1;
+    uint32_t first = 0;
+    if (n < iters) {
+      if ((q & 1) == 0) {
+        const uint32_t j = (uint32_t)(begin + n * NT) + tok;
+        there = (uint32_t)page < a.num_pages;
+        src_row = there ? ((uint64_t)(uint32_t)page * a.heads + hk) * a.page_size + (j - a.by_page.div(j) * a.page_size) : 0;
+        page_of(n + 1);
+      }
+      // a token that is not there gets row 0's codes, and zero scales when decoded (finite: P = 0 meets them)
+      first = W::fetch(a, q & 1 ? a.codes[1] : a.codes[0], q & 1 ? a.scales[1] : a.scales[0], src_row, e0, sbase + S::at_raw + (q & 1) * S::raw, p) | (there ? 4u : 0u);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return first;
+  };
+  uint32_t cur = 0, next = 0;
+  if (warp < W_MMA) {
+    page_of(0);
+    cur = fetch(0);
+    next = fetch(1);
+  }
   // pages out of range: the softmax then looks every token up
   int bad = 0;
-  if (iters > 0) {
+  if (iters > 0 && warp < W_SOFT) {  // the softmax warps have the queries to bring in
     const uint32_t pg0 = a.by_page.div((uint32_t)max(begin, rg.lo)), pg1 = a.by_page.div((uint32_t)(end - 1));
-    for (uint32_t pg = pg0 + threadIdx.x; pg <= pg1; pg += THREADS) bad |= (uint32_t)__ldg(table + pg) >= a.num_pages;
+    for (uint32_t pg = pg0 + threadIdx.x; pg <= pg1; pg += W_SOFT * 32) bad |= (uint32_t)__ldg(table + pg) >= a.num_pages;
     if (bad) atomicOr(&g_device_error, (unsigned)kDevErrIndex);
   }
   // softmax warps: their query tile, half of the tokens, row of the tile
   const int qt = (warp - W_SOFT) >> 3, half = (warp >> 2) & 1;
   const uint32_t row = (uint32_t)(threadIdx.x & 127u);
   const uint32_t r = r0 + 128u * qt + row;
-  float fz = 0.0f;
   const bool softmax = warp >= W_SOFT && qt < nq;
-  if (softmax) {  // either thread of a row stores half of it
-    const uint32_t i = min(r, R - 1u) / a.G, h = hk * a.G + (min(r, R - 1u) - i * a.G);
-    const QT* q = static_cast<const QT*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * a.D;
-    float mx = 0.0f;
-    for (uint32_t k = 0; k < a.D; k += 8) {
-      float x[8];
-      load8<QT>(q + k, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-    }
-    const int e2 = mx > 0.0f ? max(-80, (int)((__float_as_uint(mx) >> 23) & 255u) - 127) : 0;
-    constexpr int up2 = kMx ? 16 : 14;
-    const float up = pow2(up2 - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
+  if (softmax) {
+    // A warp brings 16 rows of the queries in, an octet a lane, so that a load
+    // reads whole rows (a row a thread kept the load unit busy for 2 us a tile).
+    constexpr uint32_t OPR = DP / 8, RPI = 32 / OPR;  // octets of a row, rows a load
+    constexpr int LOADS = 16 / RPI, NB = LOADS < 8 ? LOADS : 8;
+    const uint32_t o = (uint32_t)lane % OPR;
     const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
-    fz = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(Mx<MODE>::key_down - up2), 1e-37f);
-    for (uint32_t o = half; o < a.D / 8u; o += 2u) {
-      float x[8];
-      load8<QT>(q + 8u * o, x);
-      uint32_t v[4];
+#pragma unroll 1
+    for (int k0 = 0; k0 < LOADS; k0 += NB) {
+      uint4 raw[NB];
+      const uint32_t rr0 = 16u * ((uint32_t)(warp - W_SOFT) & 7u) + RPI * k0 + (uint32_t)lane / OPR;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y0 = x[octet<MODE>(2 * e)] * up, y1 = x[octet<MODE>(2 * e + 1)] * up;
-        v[e] = kMx ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
+      for (int k = 0; k < NB; ++k) {
+        const uint32_t rq = min(r0 + 128u * qt + rr0 + RPI * k, R - 1u), i = rq / a.G, h = hk * a.G + (rq - i * a.G);
+        const QT* q = static_cast<const QT*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * a.D;
+        raw[k] = o < a.D / 8u ? __ldg(reinterpret_cast<const uint4*>(q) + o) : make_uint4(0, 0, 0, 0);
       }
-      st_shared_v4(sq + qt * S::q_tile + (row >> 3) * S::group + (o >> 3) * 1024u + (row & 7u) * 128u + (((o & 7u) ^ (row & 7u)) << 4),
-                   make_uint4(v[0], v[1], v[2], v[3]));
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const uint32_t rr = rr0 + RPI * k;
+        float x[8], mx = 0.0f;
+        unpack8<QT>(raw[k], raw[k], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (uint32_t d = OPR / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const int e2 = mx > 0.0f ? max(-80, (int)((__float_as_uint(mx) >> 23) & 255u) - 127) : 0;
+        constexpr int up2 = kMx ? 16 : 14;
+        const float up = pow2(up2 - e2) * (a.scale < 0.0f ? -1.0f : 1.0f);
+        if (o == 0) row_factor[qt][rr] = fmaxf(fabsf(a.scale) * kLog2e * pow2(e2) * gk * pow2(Mx<MODE>::key_down - up2), 1e-37f);
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y0 = x[octet<MODE>(2 * e)] * up, y1 = x[octet<MODE>(2 * e + 1)] * up;
+          v[e] = kMx ? pack_bf16x2(y0, y1) : pack_f16x2(y0, y1);
+        }
+        if (o < a.D / 8u)
+          st_shared_v4(sq + qt * S::q_tile + (rr >> 3) * S::group + (o >> 3) * 1024u + (rr & 7u) * 128u + (((o & 7u) ^ (rr & 7u)) << 4),
+                       make_uint4(v[0], v[1], v[2], v[3]));
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -378,35 +427,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
 
   if (warp < W_MMA) {
     // ------------------------------------------------------------ producers
-    using W = Raw<MODE, DP>;
-    const uint32_t p = threadIdx.x, tok = p % NT, e0 = p / NT * S::EPT;
-    // tile n's token: its page number is loaded a tile before its row is
-    // wanted, its codes and scales a tile before they are decoded
-    int32_t page = -1;
-    auto page_of = [&](int32_t n) {
-      const int32_t j = begin + n * NT + (int32_t)tok;
-      page = n < iters && j >= rg.lo && j < end ? __ldg(table + a.by_page.div((uint32_t)j)) : -1;
-    };
-    uint64_t row = 0;
-    bool there = false;
-    auto fetch = [&](int32_t q) {  // tile q / 2, side q % 2
-      const int32_t n = q >> 1;
-      uint32_t first = 0;
-      if (n < iters) {
-        if ((q & 1) == 0) {
-          const uint32_t j = (uint32_t)(begin + n * NT) + tok;
-          there = (uint32_t)page < a.num_pages;
-          row = there ? ((uint64_t)(uint32_t)page * a.heads + hk) * a.page_size + (j - a.by_page.div(j) * a.page_size) : 0;
-          page_of(n + 1);
-        }
-        // a token that is not there gets row 0's codes, and zero scales when decoded (finite: P = 0 meets them)
-        first = W::fetch(a, q & 1 ? a.codes[1] : a.codes[0], q & 1 ? a.scales[1] : a.scales[0], row, e0, sbase + S::at_raw + (q & 1) * S::raw, p) | (there ? 4u : 0u);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      return first;
-    };
-    page_of(0);
-    uint32_t cur = fetch(0), next = fetch(1);
 #pragma unroll 1
     for (int32_t q = 0; q < 2 * iters; ++q) {
       const uint32_t side = (uint32_t)q & 1u, n = (uint32_t)q >> 1, nst = side ? S::st_v : S::st_k;
@@ -493,6 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     const uint32_t tl = tmem + ((32u * ((uint32_t)warp & 3u)) << 16);
     const uint32_t ts_ = tl + S::tm_s + 128u * qt + S::HC * half, to = tl + S::tm_o + 128u * qt;
     const uint32_t i = min(r, R - 1u) / a.G;
+    const float fz = row_factor[qt][row];
     const Range see = TREE ? tree_range(a, s, i) : tile_range(a, s, i, i);
     const uint32_t f0 = r0 + 128u * qt, f1 = min(f0 + 127u, R - 1u);
     int32_t all_lo = tile_range(a, s, f1 / a.G, f1 / a.G).lo, all_hi = min(end, tile_range(a, s, f0 / a.G, f0 / a.G).hi);
