@@ -577,7 +577,7 @@ NVFP4_API nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, 
  * query's place in its branch.  The window hides no drafts.
  * tree_mask [T, mask_words] uint32, a row for each query token;
  * 32*mask_words >= min(max_q, T), mask_words <= 2^20.  q_start is needed.
- * Everything else, the workspace and its size included, as in kv_attention. */
+ * Everything else as in kv_attention. */
 NVFP4_API nvfp4_status kv_attention_tree(const nvfp4_kv_cache* cache, const void* q, nvfp4_dtype q_dt,
                                          int64_t q_stride, const int32_t* q_start, const int32_t* kv_len,
                                          const int32_t* page_table, const uint32_t* tree_mask, int64_t mask_words,
@@ -585,11 +585,15 @@ NVFP4_API nvfp4_status kv_attention_tree(const nvfp4_kv_cache* cache, const void
                                          int64_t max_pages, float scale, int64_t window, void* out, float* lse,
                                          void* workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
-/* Bytes of workspace with which kv_attention and kv_attention_tree split as
- * they would choose to, for a cache of `heads` heads of D; 0 when it would not split (or for sizes
+/* Bytes of workspace with which kv_attention splits as it would choose to,
+ * for a cache of `heads` heads of D; 0 when it would not split (or for sizes
  * it rejects).  Host only. */
 NVFP4_API size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D,
                                              int64_t max_q, int64_t max_kv, int64_t window);
+
+/* The same of kv_attention_tree. */
+NVFP4_API size_t kv_attention_tree_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D,
+                                                  int64_t max_q, int64_t max_kv, int64_t window);
 
 #ifdef __cplusplus
 }

@@ -1267,8 +1267,7 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   p.chunk = p.chunks = 1;
   if (!p.prefill) {
     // D 256: two n-tiles would take more registers than there are; trees of so
-    // few rows are rare and have no variant of their own (the workspace of 8-row
-    // tiles then has room for two workers an SM, as many as are resident)
+    // few rows are rare and have no variant of their own
     p.tile_rows = (rows <= 8 && !tree) || D > 128 ? 8 : 16;
     p.bytes_per_chunk = (size_t)(2 * p.tile_rows * (D * 4 + 8) + 32);
     return p;
@@ -1283,6 +1282,22 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   int64_t chunk = share < (double)span ? (int64_t)share + 1 : span;
   int64_t fit = workspace_bytes == SIZE_MAX ? span : (int64_t)(workspace_bytes / p.bytes_per_chunk);
   if (fit < 2) fit = 1;
+  if (tree) {
+    // Few row tiles: as many chunks as take the least time, in tiles of 128
+    // tokens (2.8 us): a CTA costs 5 of them besides its own, the join 3.  (144
+    // row tiles over 4160 tokens: 113 us whole, 186 in chunks of 4096.)
+    double best = 0;
+    for (int64_t c = 1; c <= 64 && c <= fit && (c - 1) * 128 < (span > 0 ? span : 1); ++c) {
+      const int64_t each = ((span + c - 1) / c + 127) / 128;
+      const double waves = tiles * (double)c / 148, t = (waves > (double)(int64_t)waves ? (int64_t)waves + 1 : (int64_t)waves) * (5.0 + each) + (c > 1 ? 3.0 : 0.0);
+      if (c == 1 || t < best) {
+        best = t;
+        p.chunk = each > 0 ? each * 128 : 128;
+      }
+    }
+    p.chunks = span > 0 ? (span + p.chunk - 1) / p.chunk : 1;
+    return p;
+  }
   if ((span + fit - 1) / fit > chunk) chunk = (span + fit - 1) / fit;
   p.chunk = (chunk + 127) / 128 * 128;
   if (p.chunk < 512) p.chunk = 512;
@@ -1290,21 +1305,31 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   return p;
 }
 
-size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q,
-                                   int64_t max_kv, int64_t window) {
+static size_t kv_workspace(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q, int64_t max_kv,
+                           int64_t window, bool tree) {
   if (B < 1 || B > 65535 || T < 1 || T > (1 << 30) || heads < 1 || heads > 65535 || Hq < 1 || Hq > 65535 ||
       Hq % heads != 0 || D < 32 || D > 256 || D % 32 != 0 || max_q < 1 || max_q > (1 << 30) || max_kv < 0 ||
       max_kv > (1 << 30) || window < 0 || product_exceeds(T, Hq * D, kMaxElems))
     return 0;
   size_t most = 0;  // over the kernels that the types may choose
   for (int i = 0; i < 2; ++i) {
-    const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, false, SIZE_MAX);
+    const KvPlan p = kv_plan(B, T, Hq, heads, D, max_q, max_kv, window > (1 << 30) ? 0 : window, i != 0, tree, SIZE_MAX);
     // 64 tokens are one unit of work: nothing to split
     const size_t bytes = p.prefill ? (p.chunks > 1 ? p.chunks * p.bytes_per_chunk : 0)
                                    : (max_kv > 64 ? (size_t)kKvMaxWorkers * p.bytes_per_chunk : 0);
     if (bytes > most) most = bytes;
   }
   return most;
+}
+
+size_t kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q,
+                                   int64_t max_kv, int64_t window) {
+  return kv_workspace(B, T, Hq, heads, D, max_q, max_kv, window, false);
+}
+
+size_t kv_attention_tree_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D, int64_t max_q,
+                                        int64_t max_kv, int64_t window) {
+  return kv_workspace(B, T, Hq, heads, D, max_q, max_kv, window, true);
 }
 
 // kv_attention, and with masks over the queries' own tokens kv_attention_tree.

@@ -87,6 +87,7 @@ SIGNATURES = [
     ("kv_attention", _I, [ctypes.POINTER(KvCacheArgs), _P, _I, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                           ctypes.c_float, _I, _I64, _P, _P, _P, _SZ, _P]),
     ("kv_attention_workspace_size", _SZ, [_I64] * 8),
+    ("kv_attention_tree_workspace_size", _SZ, [_I64] * 8),
 ]
 
 _lib = None
@@ -895,6 +896,12 @@ def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_l
     return out if lse is None else (out, lse)
 
 
+@functools.lru_cache(maxsize=4096)
+def kv_attention_tree_workspace_size(B: int, T: int, Hq: int, heads: int, D: int, max_q: int = 1, max_kv: int = 0,
+                                     window: int = 0) -> int:
+    return int(lib().kv_attention_tree_workspace_size(B, T, Hq, heads, D, max_q, max_kv, window))
+
+
 def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
                       tree_mask: torch.Tensor, q_start: torch.Tensor, max_q: int | None = None, max_kv: int | None = None,
                       scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
@@ -905,7 +912,9 @@ def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
     of tree_mask [T, words] int32 (bit d % 32 of word d / 32: draft d, itself
     included only where its bit is set; 32 * words >= max_q).  window: the
     context within window tokens of the query's place in its branch (the number
-    of drafts it sees, less one).  The rest as in kv_attention."""
+    of drafts it sees, less one).  workspace: uint8 scratch of
+    kv_attention_tree_workspace_size bytes (allocated here when None).  The rest
+    as in kv_attention."""
     T, Hq, D = q.shape
     B, max_pages = page_table.shape
     # (what is None is not looked at: a decoding call is short)
@@ -942,7 +951,7 @@ def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
     if lse is None and return_lse:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     if workspace is None:
-        size = kv_attention_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
+        size = kv_attention_tree_workspace_size(B, T, Hq, cache.heads, cache.D, max_q, max_kv, window)
         workspace = torch.empty(size, dtype=torch.uint8, device=cache.device) if size else None
     else:
         size = _nbytes(workspace)

@@ -64,7 +64,7 @@ def test_long_contexts_split_and_whole(nv, mode, n, G):
     c, t = make(nv, mode, lens, 2, 128, 16, 3)
     q = seeded((2 * n, 2 * G, 128), 5, bf16)
     masks = ancestors(n, 1) + ancestors(n, 2)
-    size = nv.kv_attention_workspace_size(2, 2 * n, 2 * G, 2, 128, n, 3000)
+    size = nv.kv_attention_tree_workspace_size(2, 2 * n, 2 * G, 2, 128, n, 3000)
     assert size > 0
     for b in (size, size // 2, 0):
         compare_tree(nv, c, t, lens, [n, n], q, masks, max_kv=3000, workspace=torch.empty(b, dtype=torch.uint8, device="cuda"))

@@ -135,7 +135,8 @@ def test_the_binding_passes_masks_on(monkeypatch):
     seen = []
     real = nv.lib()
     fake = types.SimpleNamespace(kv_attention=lambda *a: seen.append(("plain", a)) or 0, kv_attention_tree=lambda *a: seen.append(("tree", a)) or 0,
-                                 kv_attention_workspace_size=real.kv_attention_workspace_size)
+                                 kv_attention_workspace_size=real.kv_attention_workspace_size,
+                                 kv_attention_tree_workspace_size=real.kv_attention_tree_workspace_size)
     monkeypatch.setattr(nv, "lib", lambda: fake)
     i = torch.int32
     q, table, n, starts, mask = e(5, 4, 64, dtype=torch.bfloat16), e(1, 4, dtype=i), e(1, dtype=i), e(2, dtype=i), e(5, 3, dtype=i)
@@ -146,3 +147,25 @@ def test_the_binding_passes_masks_on(monkeypatch):
     assert a[:7] == t[:7] and t[7:9] == (mask.data_ptr(), 3) and a[7:14] == t[9:16]
     assert a[7:14] == (1, 5, 4, 5, 60, 4, 64 ** -0.5) and a[14:16] == (False, 7) and t[16] == 7
     assert t[17] == out.data_ptr() and t[18] == lse.data_ptr()
+
+
+@pytest.mark.parametrize("args,want", [
+    # B, T, Hq, heads, D, max_q, max_kv, window; up to 32 rows k_kv_decode's tiles of 16: 592 workers, two partial results each
+    ((1, 8, 32, 8, 128, 8, 1000), 592 * (2 * 16 * (4 * 128 + 8) + 32)),
+    ((1, 1, 32, 8, 128, 1, 1000), 592 * (2 * 16 * (4 * 128 + 8) + 32)),
+    ((1, 8, 32, 8, 128, 8, 64), 0),                      # one unit of tokens: nothing to split
+    # 8 row tiles of 256: 16 chunks of 512 tokens, 128 CTAs of 5 + 4 tiles' time and the join's 3
+    ((1, 64, 32, 8, 128, 64, 8192), 16 * 64 * 32 * (4 * 128 + 8)),
+    # 144 row tiles fill the GPU: no chunks (what is left is k_kv_decode's, for types that k_kv_prefill does not take)
+    ((18, 18 * 64, 32, 8, 128, 64, 4160), 592 * (2 * 16 * (4 * 128 + 8) + 32)),
+])
+def test_tree_workspace_sizes(L, args, want):
+    assert nv.kv_attention_tree_workspace_size(*args) == want
+
+
+def test_tree_workspace_of_bad_sizes(L):
+    for bad in ((-1, 1, 4, 1, 64, 1, 100), (1, 1, 4, 3, 64, 1, 100), (1, 1, 4, 1, 48, 1, 100), (1, 1, 4, 1, 64, 1, -1), (1, 1, 4, 0, 64, 1, 100)):
+        assert nv.kv_attention_tree_workspace_size(*bad) == 0
+    for kv in (0, 1, 127, 128, 129, 1 << 20, 1 << 30):
+        for B, n in ((1, 64), (40, 64), (1, 5000)):
+            assert nv.kv_attention_tree_workspace_size(B, B * n, 32, 8, 128, n, kv) <= max(64 * B * n * 32 * 520, 592 * (32 * 520 + 32))
