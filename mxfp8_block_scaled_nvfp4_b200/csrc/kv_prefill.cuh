@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   __shared__ __align__(8) uint64_t full[2][2], empty[2][2], s_full[2], p_full[2], o_done[2], all_done;  // full, empty: [side][stage]
   __shared__ float other[NQ][2][128];  // maxima (later sums) that the two threads of a row exchange
   __shared__ float row_factor[NQ][128];  // logit (log2 units) of an accumulator
+  __shared__ float2 slot_ml[TREE && NQ == 2 ? 2 : 1][128];  // maxima and sums that two slots of the same rows exchange
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_flag;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -309,6 +310,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   const int32_t end = min(rg.hi, begin + a.chunk);
   const int32_t iters = end > begin ? (end - begin + NT - 1) / NT : 0;
   const int nq = NQ == 2 && r0 + 128u < R ? 2 : 1;
+  // Trees of one query tile: the second tile's S, O and threads take every other
+  // tile of tokens (slot t those of remainder t), and the two slots join at the end.
+  constexpr bool DUAL = TREE && NQ == 2;
+  const bool dual = DUAL && nq == 1 && iters > 1;
+  const int slots = dual ? 2 : nq;
   const int32_t* table = a.page_table + (uint64_t)b * a.max_pages;
   const uint32_t kchunks = a.D / 16u;
 
@@ -375,9 +381,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   // softmax warps: their query tile, half of the tokens, row of the tile
   const int qt = (warp - W_SOFT) >> 3, half = (warp >> 2) & 1;
   const uint32_t row = (uint32_t)(threadIdx.x & 127u);
-  const uint32_t r = r0 + 128u * qt + row;
-  const bool softmax = warp >= W_SOFT && qt < nq;
-  if (softmax) {
+  const uint32_t r = r0 + 128u * (dual ? 0 : qt) + row;
+  const bool softmax = warp >= W_SOFT && qt < slots;
+  if (softmax && qt < nq) {
     // A warp brings 16 rows of the queries in, an octet a lane, so that a load
     // reads whole rows (a row a thread kept the load unit busy for 2 us a tile).
     constexpr uint32_t OPR = DP / 8, RPI = 32 / OPR;  // octets of a row, rows a load
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     bool ok = true;
     auto qk = [&](int t, int32_t n) {
       if (leader) {
-        const uint64_t da = smem_desc(sq + t * S::q_tile, 16, S::group, 2);
+        const uint64_t da = smem_desc(sq + (dual ? 0 : t) * S::q_tile, 16, S::group, 2);
         const uint64_t db = smem_desc(sbase + S::at_k + ((uint32_t)n % S::st_k) * S::kv_tile, 16, S::group, 2);
         for (uint32_t j = 0; j < kchunks; ++j) {
           const uint64_t off = ((j >> 2) * 1024u + (j & 3u) * 32u) >> 4;
@@ -467,30 +473,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       tc_fence_after();
       return ok;
     };
-    if (iters > 0 && wait(full[0][0], 0)) {
+    // O of slot t, its tile number k, += P V_hat with the V tile in stage st
+    auto pv = [&](int t, int32_t k, uint32_t st) {
+      const uint64_t db = smem_desc(sbase + S::at_v + st * S::kv_tile, 1024, S::group, 2);
+      const uint32_t pa = tmem + S::tm_s + 128u * t, od = tmem + S::tm_o + 128u * t;
+      for (uint32_t j = 0; j < NT / 16; ++j) {
+        const uint64_t bj = db + ((j * 2u * S::group) >> 4);
+        const uint32_t ph = pa + S::HC * (j / (S::HC / 16u)), jh = j % (S::HC / 16u);  // P lies in its half of S
+        if constexpr (!kMx) {
+          mma_ts(od, ph + 8u * jh, bj, id_pv, (k | (int32_t)j) != 0);
+        } else {
+          const uint32_t pj = ph + 32u * (jh >> 1) + 8u * (jh & 1u);
+          mma_ts(od, pj, bj, id_pv, (k | (int32_t)j) != 0);
+          mma_ts(od, pj + 16u, bj, id_pv, 1);
+        }
+      }
+      mma_commit(smem_u32(&o_done[t]));
+    };
+    if (!dual && iters > 0 && wait(full[0][0], 0)) {
       for (int t = 0; t < nq; ++t) qk(t, 0);
       if (leader) mma_commit(smem_u32(&empty[0][0]));
     }
-    for (int32_t n = 0; n < iters && ok; ++n) {
+    for (int32_t n = 0; !dual && n < iters && ok; ++n) {
       const uint32_t st = (uint32_t)n % S::st_v, ph = ((uint32_t)n / S::st_v) & 1u;
       for (int t = 0; t < nq && ok; ++t) {
         if (t == 0 && !wait(full[1][st], ph)) break;
         if (!wait(p_full[t], (uint32_t)n & 1u)) break;
         if (leader) {
-          const uint64_t db = smem_desc(sbase + S::at_v + st * S::kv_tile, 1024, S::group, 2);
-          const uint32_t pa = tmem + S::tm_s + 128u * t, od = tmem + S::tm_o + 128u * t;
-          for (uint32_t j = 0; j < NT / 16; ++j) {
-            const uint64_t bj = db + ((j * 2u * S::group) >> 4);
-            const uint32_t ph = pa + S::HC * (j / (S::HC / 16u)), jh = j % (S::HC / 16u);  // P lies in its half of S
-            if constexpr (!kMx) {
-              mma_ts(od, ph + 8u * jh, bj, id_pv, (n | (int32_t)j) != 0);
-            } else {
-              const uint32_t pj = ph + 32u * (jh >> 1) + 8u * (jh & 1u);
-              mma_ts(od, pj, bj, id_pv, (n | (int32_t)j) != 0);
-              mma_ts(od, pj + 16u, bj, id_pv, 1);
-            }
-          }
-          mma_commit(smem_u32(&o_done[t]));
+          pv(t, n, st);
           if (t == nq - 1) mma_commit(smem_u32(&empty[1][st]));
         }
         __syncwarp();
@@ -503,6 +513,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         __syncwarp();
       }
     }
+    if constexpr (DUAL) {
+      // tile n is slot n % 2's
+      auto next_qk = [&](int32_t n) {
+        const uint32_t sn = (uint32_t)n % S::st_k;
+        if (!wait(full[0][sn], ((uint32_t)n / S::st_k) & 1u)) return;
+        qk(n & 1, n);
+        if (leader) mma_commit(smem_u32(&empty[0][sn]));
+        __syncwarp();
+      };
+      for (int32_t n = 0; dual && n < 2 && ok; ++n) next_qk(n);
+      for (int32_t n = 0; dual && n < iters && ok; ++n) {
+        const int t = n & 1;
+        const uint32_t st = (uint32_t)n % S::st_v;
+        if (!wait(full[1][st], ((uint32_t)n / S::st_v) & 1u) || !wait(p_full[t], (uint32_t)(n >> 1) & 1u)) break;
+        if (leader) {
+          pv(t, n >> 1, st);
+          mma_commit(smem_u32(&empty[1][st]));
+        }
+        __syncwarp();
+        if (n + 2 < iters) next_qk(n + 2);
+      }
+    }
     if (!ok && lane == 0) abort_flag = 1;
     // every MMA issued here has completed before TMEM is released
     if (leader) mma_commit(smem_u32(&all_done));
@@ -513,7 +545,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     const uint32_t tl = tmem + ((32u * ((uint32_t)warp & 3u)) << 16);
     const uint32_t ts_ = tl + S::tm_s + 128u * qt + S::HC * half, to = tl + S::tm_o + 128u * qt;
     const uint32_t i = min(r, R - 1u) / a.G;
-    const float fz = row_factor[qt][row];
+    const float fz = row_factor[dual ? 0 : qt][row];
+    const int32_t mine = dual ? (iters - qt + 1) / 2 : iters;  // tiles of this slot
     const Range see = TREE ? tree_range(a, s, i) : tile_range(a, s, i, i);
     const uint32_t f0 = r0 + 128u * qt, f1 = min(f0 + 127u, R - 1u);
     int32_t all_lo = tile_range(a, s, f1 / a.G, f1 / a.G).lo, all_hi = min(end, tile_range(a, s, f0 / a.G, f0 / a.G).hi);
@@ -530,8 +563,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       pair_leave(2 + 4 * qt + (warp & 3));
       return false;
     };
-    for (int32_t n = 0; n < iters; ++n) {
-      const int32_t j0 = begin + n * NT + S::HC * half;
+    for (int32_t n = 0; n < mine; ++n) {
+      const int32_t j0 = begin + (dual ? 2 * n + qt : n) * NT + S::HC * half;
       if (!__all_sync(0xffffffffu, wait_for(s_full[qt], (uint32_t)n & 1u) && !abort_flag)) {
         ok = leave();
         break;
@@ -647,29 +680,53 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
       if (lane == 0) arrive(smem_u32(&p_full[qt]));
     }
     if (ok && iters > 0) {
-      if (!__all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(iters - 1) & 1u) && !abort_flag)) ok = leave();
+      if (!__all_sync(0xffffffffu, wait_for(o_done[qt], (uint32_t)(mine - 1) & 1u) && !abort_flag)) ok = leave();
+      if (dual && ok && !__all_sync(0xffffffffu, wait_for(o_done[qt ^ 1], (uint32_t)((iters - (qt ^ 1) + 1) / 2 - 1) & 1u) && !abort_flag)) ok = leave();
       tc_fence_after();
     }
+    // A warp that gave up arrives at the slots' barrier too.
+    auto slots_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(10 + (warp & 3)) : "memory"); };
+    if (dual && !ok) asm volatile("bar.arrive %0, 128;" ::"r"(10 + (warp & 3)) : "memory");
     if (ok) {
       // the row's sum (the slots were last read before the last P)
       other[qt][half][row] = l;
       pair_sync(2 + 4 * qt + (warp & 3));
       l += other[qt][half ^ 1][row];
+      float f_mine = 1.0f, f_other = 0.0f;  // of the two slots' O
+      if (dual) {
+        if (half == 0) slot_ml[DUAL ? qt : 0][row] = make_float2(m, l);
+        slots_sync();
+        const float2 ml = slot_ml[DUAL ? qt ^ 1 : 0][row];
+        const float M = fmaxf(m, ml.x);
+        f_mine = m == -INFINITY ? 0.0f : ex2(m - M);
+        f_other = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+        l = l * f_mine + ml.y * f_other;
+        m = M;
+      }
       const uint32_t h = hk * a.G + (min(r, R - 1u) - i * a.G);
       const uint64_t at = (uint64_t)(s.t0 + i) * a.Hq + h;
       const float fv = kMx ? 1.0f : (a.g[1] ? __ldg(a.g[1]) / kGlobalEncode : 1.0f);
       const float f = whole ? (l == 0.0f ? 0.0f : fv / l) : fv;
-      if (r < R && half == 0) {
+      if (r < R && half == 0 && (!dual || qt == 0)) {
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);
         else if (a.lse) a.lse[at] = lse_of(m, l);
       }
-      for (uint32_t c = 16u * half; c < a.D; c += 32u) {
+      // 16 columns at a time, in turn over the two or four threads that have the row
+      for (uint32_t c = 16u * (dual ? 2 * qt + half : half); c < a.D; c += dual ? 64u : 32u) {
         uint32_t y[16];
         if (iters > 0) {
           tmem_ld16(to + c, y);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = 0;
+        }
+        if constexpr (DUAL) {
+          if (dual) {
+            uint32_t z[16];
+            tmem_ld16(tl + S::tm_o + 128u * (qt ^ 1) + c, z);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f_mine + __uint_as_float(z[e]) * f_other);
+          }
         }
         if (r < R)
 #pragma unroll

@@ -57,7 +57,9 @@ def test_trees(nv, mode, dtype, heads, G, D, page_size):
         compare_tree(nv, c, t, lens, n, q, masks, window=37)
 
 
-@pytest.mark.parametrize("mode,n,G", [("nvfp4", 6, 4), ("nvfp4", 40, 4), ("mxfp8", 6, 4), ("mxfp4", 40, 4)])
+# 24 rows; 80 and 128 (one query tile, whose tokens two slots take in turn); 160
+@pytest.mark.parametrize("mode,n,G", [("nvfp4", 6, 4), ("nvfp4", 20, 4), ("nvfp4", 32, 4), ("nvfp4", 40, 4), ("mxfp8", 6, 4), ("mxfp8", 20, 4),
+                                      ("mxfp4", 32, 4), ("mxfp4", 40, 4)])
 def test_long_contexts_split_and_whole(nv, mode, n, G):
     """Contexts cut over many workers, with all, some and none of the workspace."""
     lens = [3000, 1033]
