@@ -141,7 +141,7 @@ def _need_cuda(*ts):
     """Every tensor is a contiguous CUDA tensor on the current device: the
     library launches on the current device and the current stream, so a
     tensor of another GPU would be read through a pointer that GPU's kernels
-    cannot use."""
+    cannot use.  Returns that device (None without a tensor)."""
     dev = None
     for t in ts:
         if t is not None:
@@ -154,6 +154,7 @@ def _need_cuda(*ts):
             if t.device.index != dev:
                 raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}; "
                                  "call under torch.cuda.device(tensor.device)")
+    return dev
 
 
 def _nbytes(t) -> int:
@@ -553,27 +554,35 @@ def gather_qmm_noalloc(x, w_codes, w_scales, g, idx, out=None) -> torch.Tensor:
 # ---------------------------------------------------------------------------
 # root-mean-square norm
 # ---------------------------------------------------------------------------
-def _need_norm(x, w, residual, h, rstd):
-    """Types and sizes of a norm's tensors; (rows, K) of x [..., K]."""
-    if x.dtype not in DT:
+def _need_norm(x, w, residual, h, rstd, *more):
+    """Types and sizes of a norm's tensors; (rows, K, device) of x [..., K].
+    (These calls are short: what is in order costs one comparison.)"""
+    dtype = x.dtype
+    if dtype not in DT:
         raise ValueError("x must be float32, float16 or bfloat16")
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
-    _need_dtype(w, x.dtype, "weight")
-    if w.numel() != K:
+    if w.dtype != dtype or w.numel() != K:
+        _need_dtype(w, dtype, "weight")
         raise ValueError(f"weight must hold {K} elements, got {w.numel()}")
-    for t, what in ((residual, "residual"), (h, "h")):
-        _need_dtype(t, x.dtype, what)
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{what} must be {tuple(x.shape)}, got {tuple(t.shape)}")
-    if h is not None and residual is None:
+    if residual is not None:
+        _need_like(residual, x, "residual")
+        if h is not None:
+            _need_like(h, x, "h")
+    elif h is not None:
         raise ValueError("h is given with a residual, and only then")
-    _need_dtype(rstd, torch.float32, "rstd")
-    _need_bytes(rstd, 4 * rows, "rstd")
-    _need_cuda(x, w, residual, h, rstd)
-    return rows, K
+    if rstd is not None:
+        _need_dtype(rstd, torch.float32, "rstd")
+        _need_bytes(rstd, 4 * rows, "rstd")
+    return rows, K, _need_cuda(x, w, residual, h, rstd, *more)
+
+
+def _need_like(t, x, what: str):
+    _need_dtype(t, x.dtype, what)
+    if t.shape != x.shape:
+        raise ValueError(f"{what} must be {tuple(x.shape)}, got {tuple(t.shape)}")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -584,17 +593,19 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     shape [..., K]; with return_rstd (or an rstd tensor) the triple (y, h,
     rstd), rstd fp32 [rows] for rms_norm_vjp.  h may be x or residual, to add
     in place."""
-    rows, K = _need_norm(x, weight, residual, h, rstd)
-    _need_dtype(out, x.dtype, "out")
-    _need_bytes(out, _nbytes(x), "out")
-    _need_cuda(out)
-    out = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _need_dtype(out, x.dtype, "out")
+        _need_bytes(out, _nbytes(x), "out")
+    rows, K, dev = _need_norm(x, weight, residual, h, rstd, out)
+    if out is None:
+        out = torch.empty_like(x)
     if residual is not None and h is None:
         h = torch.empty_like(x)
     if rstd is None and return_rstd:
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _check(lib().rms_norm(_ptr(x), _ptr(residual), _ptr(weight), DT[x.dtype], rows, K, eps, _ptr(h), _ptr(out), _ptr(rstd),
-                          _stream()))
+    _check(lib().rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), DT[x.dtype], rows, K,
+                          eps, None if h is None else h.data_ptr(), out.data_ptr(), None if rstd is None else rstd.data_ptr(),
+                          _raw_stream(dev)))
     y = (out, x if h is None else h)
     return y if rstd is None else y + (rstd,)
 
@@ -609,26 +620,32 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, mode: str, g: torch
     return_rstd (or an rstd tensor) rstd as well."""
     if mode not in MODE:
         raise ValueError("rms_norm_quantize: mode must be nvfp4, mxfp8 or mxfp4")
-    rows, K = _need_norm(x, weight, residual, h, rstd)
+    if g is not None:
+        _need_g(g, 1, "g")
+    rows, K, dev = _need_norm(x, weight, residual, h, rstd, g, codes, scales)
     per, group = 4 if mode == "mxfp8" else 8, 16 if mode == "nvfp4" else 32
-    _need_g(g, 1, "g")
-    _need_bytes(codes, rows * (K // per) * 4, "codes")
-    _need_bytes(scales, _scale_nbytes(rows, K // group, layout), "scales")
-    _need_cuda(g, codes, scales)
     if codes is None:
         codes = torch.empty(rows, K // per, dtype=torch.int32, device=x.device)
+    else:
+        _need_bytes(codes, rows * (K // per) * 4, "codes")
+    shape = scale_shape(rows, K // group, layout)
     if scales is None:
-        scales = torch.empty(scale_shape(rows, K // group, layout), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    else:
+        _need_bytes(scales, shape[0] * shape[1], "scales")
     if residual is not None and h is None:
         h = torch.empty_like(x)
     if rstd is None and return_rstd:
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _check(lib().rms_norm_quantize(MODE[mode], _ptr(x), _ptr(residual), _ptr(weight), DT[x.dtype], rows, K, eps, _ptr(g),
-                                   _ptr(h), _ptr(codes), _ptr(scales), LAYOUT[layout], _ptr(rstd), _stream()))
+    _check(lib().rms_norm_quantize(
+        MODE[mode], x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), DT[x.dtype], rows, K, eps,
+        None if g is None else g.data_ptr(), None if h is None else h.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+        LAYOUT[layout], None if rstd is None else rstd.data_ptr(), _raw_stream(dev)))
     y = (codes, scales, x if h is None else h)
     return y if rstd is None else y + (rstd,)
 
 
+@functools.lru_cache(maxsize=4096)
 def rms_norm_vjp_workspace_size(rows: int, K: int) -> int:
     return int(lib().rms_norm_vjp_workspace_size(rows, K))
 
@@ -641,21 +658,23 @@ def rms_norm_vjp(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: 
     rstd as the forward call gave them; dh: gradient that reaches h past the
     norm (None: none).  dx (dy's dtype; it may be dy or dh) is the gradient of
     x and of residual; dw fp32 [K] that of weight."""
-    rows, K = _need_norm(dy, weight, dh, None, rstd)
-    _need_dtype(h, dy.dtype, "h")
-    if h.shape != dy.shape:
-        raise ValueError(f"h must be {tuple(dy.shape)}, got {tuple(h.shape)}")
-    _need_dtype(dx, dy.dtype, "dx")
-    _need_bytes(dx, _nbytes(dy), "dx")
-    _need_dtype(dw, torch.float32, "dw")
-    _need_bytes(dw, 4 * K, "dw")
-    _need_cuda(h, dx, dw, workspace)
-    dx = torch.empty_like(dy) if dx is None else dx
-    dw = torch.empty(K, dtype=torch.float32, device=dy.device) if dw is None else dw
+    _need_like(h, dy, "h")
+    if dx is not None:
+        _need_dtype(dx, dy.dtype, "dx")
+        _need_bytes(dx, _nbytes(dy), "dx")
+    rows, K, dev = _need_norm(dy, weight, dh, None, rstd, h, dx, dw, workspace)
+    if dw is not None:
+        _need_dtype(dw, torch.float32, "dw")
+        _need_bytes(dw, 4 * K, "dw")
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dw is None:
+        dw = torch.empty(K, dtype=torch.float32, device=dy.device)
     if workspace is None:
         workspace = torch.empty(rms_norm_vjp_workspace_size(rows, K), dtype=torch.uint8, device=dy.device)
-    _check(lib().rms_norm_vjp(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), DT[dy.dtype], rows, K, _ptr(dx),
-                              _ptr(dw), _ptr(workspace), _nbytes(workspace), _stream()))
+    _check(lib().rms_norm_vjp(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), None if dh is None else dh.data_ptr(),
+                              DT[dy.dtype], rows, K, dx.data_ptr(), dw.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                              _raw_stream(dev)))
     return dx, dw
 
 
@@ -692,7 +711,7 @@ class KvCache:
         args = KvCacheArgs(MODE[mode], P, R, H, D, *(None if t is None else t.data_ptr() for t in (
             k_codes, k_scales, v_codes, v_scales, g_k, g_v)))
         self.__dict__.update(mode=mode, num_pages=P, heads=H, page_size=R, D=D, k_codes=k_codes, k_scales=k_scales,
-                             v_codes=v_codes, v_scales=v_scales, g_k=g_k, g_v=g_v, device=k_codes.device, _args=args,
+                             v_codes=v_codes, v_scales=v_scales, g_k=g_k, g_v=g_v, device=k_codes.device, _index=k_codes.device.index, _args=args,
                              _ref=ctypes.byref(args))
 
     def __setattr__(self, name, value):
@@ -718,7 +737,7 @@ class KvCache:
 def _need_rows(t, shape, what: str, dev: int):
     """[T, heads, D] on the current device `dev`, heads and D contiguous, any
     token stride (a part of a longer row is taken as it is)."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
@@ -734,7 +753,7 @@ def _need_rows(t, shape, what: str, dev: int):
 def _need_cache(cache) -> int:
     """The current device, which has to be the cache's."""
     dev = torch.cuda.current_device()
-    if cache.device.index != dev:
+    if cache._index != dev:
         raise ValueError(f"the cache is on {cache.device}, but the current device is cuda:{dev}; "
                          "call under torch.cuda.device(cache.device)")
     return dev
@@ -767,7 +786,8 @@ def kv_cache_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.T
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     Hq = q.shape[1]
-    if q.dtype != k.dtype or k.dtype != v.dtype or k.dtype not in DT:
+    dtype = q.dtype
+    if dtype != k.dtype or dtype != v.dtype or dtype not in DT:
         raise ValueError("q, k and v must share a dtype: float32, float16 or bfloat16")
     _need_dtype(slots, torch.int32, "slots")
     _need_dtype(positions, torch.int32, "positions")
@@ -775,18 +795,20 @@ def kv_cache_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.T
     _need_dtype(sin, torch.float32, "sin")
     if cos.dim() != 2 or cos.shape != sin.shape:
         raise ValueError("cos and sin must both be [max_pos, rot / 2]")
-    _need_bytes(positions, 4 * T, "positions")
+    if positions.numel() < T:
+        _need_bytes(positions, 4 * T, "positions")
     if q_out is not None:
-        _need_dtype(q_out, q.dtype, "q_out")
+        _need_dtype(q_out, dtype, "q_out")
         _need_bytes(q_out, T * Hq * D * q.element_size(), "q_out")
     _need_cuda(slots, positions, cos, sin, q_out)
-    dev = _need_cache(cache)
-    strides = (_need_rows(q, (T, Hq, D), "q", dev), _need_rows(k, (T, heads, D), "k", dev), _need_rows(v, (T, heads, D), "v", dev))
+    dev, shape = _need_cache(cache), (T, heads, D)
+    q_stride, k_stride, v_stride = _need_rows(q, (T, Hq, D), "q", dev), _need_rows(k, shape, "k", dev), _need_rows(v, shape, "v", dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
-    _check(lib().kv_cache_append(cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), DT[q.dtype], T, Hq, *strides,
-                                 cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], interleaved,
-                                 positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), _stream()))
+        q_out = torch.empty((T, Hq, D), dtype=dtype, device=cache.device)
+    most, half = cos.shape
+    _check(lib().kv_cache_append(cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), DT[dtype], T, Hq, q_stride, k_stride, v_stride,
+                                 cos.data_ptr(), sin.data_ptr(), most, 2 * half, interleaved, positions.data_ptr(),
+                                 slots.data_ptr(), q_out.data_ptr(), _raw_stream(dev)))
     return q_out
 
 
@@ -804,9 +826,9 @@ def kv_cache_move(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, starts: 
     if starts is not None and (starts.dim() != 1 or starts.shape[0] < 1):
         raise ValueError("starts must be [S + 1]")
     _need_cuda(src, dst, starts)
-    _need_cache(cache)
+    dev = _need_cache(cache)
     _check(lib().kv_cache_move(cache._ref, src.data_ptr(), dst.data_ptr(), M, None if starts is None else starts.data_ptr(),
-                               M if starts is None else starts.shape[0] - 1, _stream()))
+                               M if starts is None else starts.shape[0] - 1, _raw_stream(dev)))
 
 
 def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None):
@@ -821,12 +843,12 @@ def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_o
     if k_out.dtype != v_out.dtype or k_out.dtype not in DT:
         raise ValueError("k_out and v_out must share a dtype: float32, float16 or bfloat16")
     for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
     _need_cuda(slots, k_out, v_out)
-    _need_cache(cache)
+    dev = _need_cache(cache)
     _check(lib().kv_cache_read(cache._ref, slots.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(),
-                               DT[k_out.dtype], _stream()))
+                               DT[k_out.dtype], _raw_stream(dev)))
     return k_out, v_out
 
 
