@@ -73,18 +73,13 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, uint32_t u) {
   const uint32_t t = a.q_per_token.div(u), y = u - t * a.q_per_token.d;
   const uint32_t grp = a.r.per_head.div(y), j = y - grp * a.r.per_head.d;
   const int32_t slot = __ldg(a.r.slots + t), pos = __ldg(a.positions + t);
-  if (slot < 0) return;
-  if ((uint32_t)slot >= a.r.num_slots || (uint32_t)pos >= a.max_pos) {
-    atomicOr(&g_device_error, (unsigned)kDevErrIndex);
-    return;
-  }
   const uint32_t half = a.rot / 2u, D = a.r.D, h0 = grp * HEADS;
   const bool turns = j * 16u < a.rot, pairs = turns && !a.interleaved;
   const uint32_t e0 = pairs ? j * 8u : j * 16u, e1 = pairs ? e0 + half : e0 + 8u;
   const T* q = static_cast<const T*>(a.q) + (int64_t)t * a.q_stride + (int64_t)h0 * D;
   T* out = static_cast<T*>(a.q_out) + ((int64_t)t * a.Hq + h0) * D;
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  uint4 x[HEADS][2][W];
+  uint4 x[HEADS][2][W];  // (loaded beside slot and position, which may yet say that the token is skipped)
 #pragma unroll
   for (int h = 0; h < HEADS; ++h)
     if (h0 + h < a.Hq)
@@ -93,6 +88,11 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, uint32_t u) {
         x[h][0][w] = __ldg(reinterpret_cast<const uint4*>(q + h * D + e0) + w);
         x[h][1][w] = __ldg(reinterpret_cast<const uint4*>(q + h * D + e1) + w);
       }
+  if (slot < 0) return;
+  if ((uint32_t)slot >= a.r.num_slots || (uint32_t)pos >= a.max_pos) {
+    atomicOr(&g_device_error, (unsigned)kDevErrIndex);
+    return;
+  }
   float c[8], s[8];
   if (turns) {
     load8<float>(a.cs[0] + (uint64_t)pos * half + j * 8u, c);
@@ -141,23 +141,19 @@ __global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant
   const uint32_t u = (blockIdx.x - a.q_ctas - side * a.kv_ctas) * kRowThreads + threadIdx.x;
   const bool in = u < a.r.units;
   const Unit w = unit_at(a.r, in ? u : 0u);
+  const T* head = static_cast<const T*>(a.r.x[side]) + (int64_t)w.t * a.r.stride[side] + (int64_t)w.h * a.r.D;
+  RawBlk<T> raw;
+  load_blk<T, V8>(head + w.j * 16u, raw);
   const int32_t slot = in ? __ldg(a.r.slots + w.t) : -1;
   const int32_t pos = in ? __ldg(a.positions + w.t) : 0;
   const bool bad = slot >= 0 && ((uint32_t)slot >= a.r.num_slots || (uint32_t)pos >= a.max_pos);
   if (bad) atomicOr(&g_device_error, (unsigned)kDevErrIndex);
   const bool go = slot >= 0 && !bad;
   float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  if (go) {
-    const T* head = static_cast<const T*>(a.r.x[side]) + (int64_t)w.t * a.r.stride[side] + (int64_t)w.h * a.r.D;
-    RawBlk<T> raw;
-    load_blk<T, V8>(head + w.j * 16u, raw);
-    unpack16<T>(raw, v);
-    if (side == 0) {
-      turn8<T>(a, head, (uint32_t)pos, w.j * 16u, v);
-      turn8<T>(a, head, (uint32_t)pos, w.j * 16u + 8u, v + 8);
-    }
+  unpack16<T>(raw, v);
+  if (go && side == 0) {
+    turn8<T>(a, head, (uint32_t)pos, w.j * 16u, v);
+    turn8<T>(a, head, (uint32_t)pos, w.j * 16u + 8u, v + 8);
   }
   const float E = MODE == kNV && a.r.g[side] ? kGlobalEncode / __ldg(a.r.g[side]) : 1.0f;
   uint4 q;

@@ -128,6 +128,28 @@ __device__ __forceinline__ F row_sum(F v, F* red, uint32_t row_warps, uint32_t f
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return __shfl_sync(0xffffffffu, v, 0);
 }
+// R rows' sums with one barrier; red [R][warps of a CTA].
+template <int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float (*red)[kMaxThreads / 32], uint32_t row_warps, uint32_t first) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (row_warps == 1) return;
+  const uint32_t lane = threadIdx.x & 31u;
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < R; ++k) red[k][threadIdx.x >> 5] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < R; ++k) v[k] = lane < row_warps ? red[k][first + lane] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+#pragma unroll
+  for (int k = 0; k < R; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
+}
 
 // Codes and scale byte of this lane's 16 fp32 values (MX: of the lane pair's
 // 32); all lanes call it.
@@ -278,14 +300,20 @@ __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant_
 }
 
 // The part of dw that a CTA's rows make stays in registers.  A thread has N
-// 16-byte pieces of a row, a row's threads' pieces side by side.  STAGED (N
-// pieces of 16 elements, K <= 8192): rows are copied into shared memory one or
-// two ahead, each thread's pieces into slots of its own, so that no barrier
+// 16-byte pieces of a row, a row's threads' pieces side by side.  STAGED (pieces
+// of 16 elements, K <= 8192): R rows at a time are copied into shared memory a
+// step ahead, each thread's pieces into slots of its own, so that no barrier
 // stands between copy and use; longer rows are read twice.
+// Bound by memory on many rows: 16384 x 8192 bf16 takes 169 us with its dw, 97 %
+// of the copy rate (a row at a time from registers 271, from shared memory two
+// rows ahead 202, two rows at a time 194, and with packed instructions and a
+// row's values kept from the first pass to the second, 18 instead of 34
+// instructions an element, this).  2048 x 4096 takes 16.4 us for 7.7: seven rows
+// a CTA are a chain of four steps of 2 us, and dw is 3.4 us more.
 template <typename T>
-constexpr int kVjpStages = sizeof(T) == 4 ? 2 : 3;
+constexpr int kVjpRows = sizeof(T) == 4 ? 1 : 2;  // in shared memory: two steps of 48 KB a row and stage
 template <typename T>
-constexpr uint32_t kVjpSmem = kVjpStages<T> * 3 * 16 * sizeof(T);  // bytes a thread
+constexpr uint32_t kVjpSmem = 2 * kVjpRows<T> * 3 * 16 * sizeof(T);  // bytes a thread
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -317,135 +345,221 @@ __device__ __forceinline__ uint4 piece_of_f(const float* v) {
   }
 }
 
+// Pairs of fp32 (the packed instructions round each half as the plain ones do).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// A 16-byte piece as pairs of fp32.
+template <typename T, int P>
+__device__ __forceinline__ void pairs_of(const uint4& p, float2 (&v)[P]) {
+  float x[2 * P];
+  piece_to_f<T>(p, x);
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(kMaxThreads) k_rms_norm_vjp(const __grid_constant__ VjpArgs a) {
-  constexpr int E = 16 / (int)sizeof(T), N = (STAGED ? 16 : 64) / E, ST = kVjpStages<T>;
-  extern __shared__ __align__(16) uint4 slots[];  // [stage][dy, h, dh][piece][thread]
-  __shared__ float red[2][kMaxThreads / 32];
+  constexpr int E = 16 / (int)sizeof(T), P = E / 2, N = (STAGED ? 16 : 64) / E, R = STAGED ? kVjpRows<T> : 1;
+  constexpr int H = STAGED ? N : 1;  // pieces of a row that stay in registers between its two passes
+  extern __shared__ __align__(16) uint4 slots[];  // [step % 2][row][dy, h, dh][piece][thread]
+  __shared__ float red[2][R][kMaxThreads / 32];
   const uint32_t warp = threadIdx.x >> 5, rpc = (blockDim.x >> 5) / a.row_warps;
   const uint32_t mine = warp / a.row_warps, first = mine * a.row_warps, span = a.row_warps * 32u;
   const uint32_t p0 = threadIdx.x - first * 32u, pieces = a.K / E;  // this thread's pieces: p0 + span n
-  const uint4* src[3] = {static_cast<const uint4*>(a.dy), static_cast<const uint4*>(a.h), static_cast<const uint4*>(a.dh)};
-  const uint4* w = static_cast<const uint4*>(a.w);
+  const uint4* w = static_cast<const uint4*>(a.w) + p0;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  const int64_t step = (int64_t)gridDim.x * rpc;
+  const int64_t next = (int64_t)gridDim.x * rpc, step = R * next;  // rows row + next k
   int64_t row = (int64_t)blockIdx.x * rpc + mine;
-  uint4 wr[STAGED ? N : 1];
-  float acc[N][E];
-  // Piece n of tensor t in a row: plain loads, dx may take dy's or dh's place.
-  auto load = [&](int64_t row, int t, int n) {
-    uint4 v = none;
-    const uint32_t p = p0 + span * n;
-    if (row < a.rows && p < pieces && (t < 2 || a.dh))
-      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src[t] + row * pieces + p));
-    return v;
-  };
-  auto slot = [&](uint32_t st, int t, int n) { return slots + ((st * 3 + t) * N + n) * blockDim.x + threadIdx.x; };
+  const uint4* src[3] = {static_cast<const uint4*>(a.dy), static_cast<const uint4*>(a.h), static_cast<const uint4*>(a.dh)};
+  bool in[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) in[n] = p0 + span * n < pieces;
+  float2 acc[N][P];
+  // slots of a step's row and tensor
+  const uint32_t mem = (uint32_t)__cvta_generic_to_shared(slots) + 16u * threadIdx.x, piece = 16u * blockDim.x;
+  auto slot = [&](uint32_t st, int k, int t, int n) { return mem + (((st * R + k) * 3 + t) * N + n) * piece; };
   auto start = [&](int64_t row, uint32_t st) {
-    if (row < a.rows)
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
-        if (t < 2 || a.dh)
+    for (int k = 0; k < R; ++k)
+      if (row + next * k < a.rows) {
+        const int64_t at = (row + next * k) * pieces + p0;
 #pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (p0 + span * n < pieces)
-              copy_async16((uint32_t)__cvta_generic_to_shared(slot(st, t, n)), src[t] + row * pieces + (p0 + span * n));
+        for (int t = 0; t < 3; ++t)
+          if (t < 2 || a.dh)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+              if (in[n]) copy_async16(slot(st, k, t, n), src[t] + at + span * n);
+      }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint32_t turn = 0, st = 0;
-  auto get = [&](int t, int n) -> uint4 {
-    if constexpr (STAGED) return row < a.rows && p0 + span * n < pieces && (t < 2 || a.dh) ? *slot(st, t, n) : none;
-    else return load(row, t, n);
+  uint32_t st = 0;
+  bool live[R] = {};
+  // piece n of tensor t in the step's row k
+  auto get = [&](int k, int t, int n) {
+    uint4 v = none;
+    if (live[k] && in[n] && (t < 2 || a.dh)) {
+      if constexpr (STAGED) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(slot(st, k, t, n)));
+      else  // plain loads: dx may take dy's or dh's place
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src[t] + row * pieces + p0 + span * n));
+    }
+    return v;
   };
-  auto weight = [&](int n) -> uint4 {
-    if constexpr (STAGED) return wr[n];
-    else return p0 + span * n < pieces ? __ldg(w + (p0 + span * n)) : none;
-  };
+  float2 wf[H][P];
+  auto weight = [&](int n) { pairs_of<T, P>(in[n] ? __ldg(w + span * n) : none, wf[n % H]); };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (STAGED) {
+    start(row, 0);
 #pragma unroll
-    for (int i = 0; i + 1 < ST; ++i) start(row + i * step, i);
-#pragma unroll
-    for (int n = 0; n < N; ++n) wr[n] = p0 + span * n < pieces ? __ldg(w + (p0 + span * n)) : none;
+    for (int n = 0; n < N; ++n) weight(n);
   }
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[n][i] = 0.0f;
+    for (int i = 0; i < P; ++i) acc[n][i] = make_float2(0.0f, 0.0f);
   const float per_k = 1.0f / (float)a.K;
-  for (int64_t base = (int64_t)blockIdx.x * rpc; base < a.rows; base += step, row += step, turn ^= 1u) {
-    const float r = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
-    if constexpr (STAGED) {
-      start(row + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+  for (int64_t base = (int64_t)blockIdx.x * rpc; base < a.rows; base += step, row += step, st ^= 1u) {
+    float r[R], s[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      live[k] = row + next * k < a.rows;
+      r[k] = live[k] ? __ldg(a.rstd + row + next * k) : 0.0f;
     }
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (STAGED) {
+      start(row + step, st ^ 1u);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
+    float2 x[R][H][P], d[R][H][P];  // h, and w dy
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float d[E], x[E], c[E];
-      piece_to_f<T>(get(0, n), d);
-      piece_to_f<T>(get(1, n), x);
-      piece_to_f<T>(weight(n), c);
+    for (int k = 0; k < R; ++k) {
+      const float2 rr = make_float2(r[k], r[k]);
+      float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        part[i & 3] = fmaf(d[i] * c[i], x[i], part[i & 3]);
-        acc[n][i] = fmaf(d[i], x[i] * r, acc[n][i]);
+      for (int n = 0; n < N; ++n) {
+        if constexpr (!STAGED) weight(n);
+        float2 y[P];
+        pairs_of<T, P>(get(k, 0, n), y);
+        pairs_of<T, P>(get(k, 1, n), x[k][n % H]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          d[k][n % H][i] = mul2(y[i], wf[n % H][i]);
+          part[i & 1] = fma2(d[k][n % H][i], x[k][n % H][i], part[i & 1]);
+          acc[n][i] = fma2(y[i], mul2(x[k][n % H][i], rr), acc[n][i]);
+        }
+      }
+      s[k] = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+    }
+    row_sums<R>(s, red[st], a.row_warps, first);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float f = s[k] * per_k * r[k] * r[k];
+      const float2 ff = make_float2(-f, -f), rr = make_float2(r[k], r[k]);
+      uint4* dx = static_cast<uint4*>(a.dx) + (row + next * k) * pieces + p0;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if constexpr (!STAGED) {
+          weight(n);
+          float2 y[P];
+          pairs_of<T, P>(get(k, 0, n), y);
+          pairs_of<T, P>(get(k, 1, n), x[k][0]);
+#pragma unroll
+          for (int i = 0; i < P; ++i) d[k][0][i] = mul2(y[i], wf[0][i]);
+        }
+        float2 g[P];
+        pairs_of<T, P>(get(k, 2, n), g);
+        float o[E];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 v = fma2(fma2(x[k][n % H][i], ff, d[k][n % H][i]), rr, g[i]);
+          o[2 * i] = v.x;
+          o[2 * i + 1] = v.y;
+        }
+        if (live[k] && in[n]) dx[span * n] = piece_of_f<T>(o);
       }
     }
-    const float s = row_sum((part[0] + part[1]) + (part[2] + part[3]), red[turn], a.row_warps, first);
-    const float f = s * per_k * r * r;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float d[E], x[E], c[E], g[E];
-      piece_to_f<T>(get(0, n), d);
-      piece_to_f<T>(get(1, n), x);
-      piece_to_f<T>(weight(n), c);
-      piece_to_f<T>(get(2, n), g);
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = fmaf(fmaf(-x[i], f, d[i] * c[i]), r, g[i]);
-      if (row < a.rows && p0 + span * n < pieces) static_cast<uint4*>(a.dx)[row * pieces + (p0 + span * n)] = piece_of_f<T>(x);
-    }
-    st = st + 1 == ST ? 0 : st + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!a.dw) return;
-  float* part = a.part + ((uint64_t)blockIdx.x * rpc + mine) * a.K;
+  // the rows that a CTA takes side by side (of at most 256 threads: 16 KB) add up in order
+  if (STAGED && rpc > 1) {
+    float4* sums = reinterpret_cast<float4*>(slots);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < P; i += 2)
+        sums[(n * P + i) / 2 * blockDim.x + threadIdx.x] = make_float4(acc[n][i].x, acc[n][i].y, acc[n][i + 1].x, acc[n][i + 1].y);
+    __syncthreads();
+    if (mine != 0) return;
+    for (uint32_t o = 1; o < rpc; ++o)
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+          const float4 v = sums[(n * P + i) / 2 * blockDim.x + o * span + threadIdx.x];
+          acc[n][i].x += v.x;
+          acc[n][i].y += v.y;
+          acc[n][i + 1].x += v.z;
+          acc[n][i + 1].y += v.w;
+        }
+  }
+  float* part = a.part + (uint64_t)blockIdx.x * a.K;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    if (p0 + span * n >= pieces) continue;
+    if (!in[n]) continue;
 #pragma unroll
-    for (int i = 0; i < E; i += 4)
-      *reinterpret_cast<float4*>(part + (p0 + span * n) * E + i) = make_float4(acc[n][i], acc[n][i + 1], acc[n][i + 2], acc[n][i + 3]);
+    for (int i = 0; i < P; i += 2)
+      *reinterpret_cast<float4*>(part + (p0 + span * n) * E + 2 * i) = make_float4(acc[n][i].x, acc[n][i].y, acc[n][i + 1].x, acc[n][i + 1].y);
   }
 }
 
-// dw: the parts added up, 32 columns a CTA (8 lanes of 4) by 32 groups of
-// parts, each group's sum in order and the groups' in order.
-__global__ void __launch_bounds__(256) k_rms_norm_dw(const __grid_constant__ VjpArgs a) {
-  __shared__ float4 sum[32][8];
-  const uint32_t c = threadIdx.x & 7u, grp = threadIdx.x >> 3, col = blockIdx.x * 32u + c * 4u;
+// dw: the parts added up, 32 columns a CTA (8 lanes of 4) by 128 groups of
+// parts; each group's parts in order, then the groups in a fixed order.
+constexpr int kDwThreads = 1024;
+__global__ void __launch_bounds__(kDwThreads) k_rms_norm_dw(const __grid_constant__ VjpArgs a) {
+  __shared__ float4 sum[kDwThreads / 32][8];
+  const uint32_t c = threadIdx.x & 7u, grp = threadIdx.x >> 3, col = blockIdx.x * 32u + c * 4u, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (col < a.K)
 #pragma unroll 4
-    for (uint32_t p = grp; p < a.parts; p += 32u) {
+    for (uint32_t p = grp; p < a.parts; p += kDwThreads / 8) {
       const float4 v = *reinterpret_cast<const float4*>(a.part + (uint64_t)p * a.K + col);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+      s[0] += v.x;
+      s[1] += v.y;
+      s[2] += v.z;
+      s[3] += v.w;
     }
-  sum[grp][c] = s;
-  __syncthreads();
-  if (grp != 0 || col >= a.K) return;
-  for (uint32_t i = 1; i < 32u; ++i) {
-    const float4 v = sum[i][c];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s[i] += __shfl_xor_sync(0xffffffffu, s[i], 8);
+    s[i] += __shfl_xor_sync(0xffffffffu, s[i], 16);
   }
-  *reinterpret_cast<float4*>(a.dw + col) = s;
+  if ((threadIdx.x & 31u) < 8u) sum[warp][c] = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (threadIdx.x >= 8u || col >= a.K) return;
+  float4 t = sum[0][c];
+#pragma unroll
+  for (int i = 1; i < kDwThreads / 32; ++i) {
+    const float4 v = sum[i][c];
+    t.x += v.x;
+    t.y += v.y;
+    t.z += v.z;
+    t.w += v.w;
+  }
+  *reinterpret_cast<float4*>(a.dw + col) = t;
 }
 
 }  // namespace norm

@@ -925,8 +925,7 @@ nvfp4_status rms_norm_quantize(nvfp4_mode mode, const void* x, const void* resid
   return rms_norm_launch(tag, mode, x, residual, w, dt, rows, K, eps, g, h, codes, scales, layout, rstd, stream);
 }
 
-// CTAs of k_rms_norm_vjp, and parts of dw (one for each row that a CTA takes
-// at a time).
+// CTAs of k_rms_norm_vjp, each with a part of dw.
 static int64_t norm_vjp_ctas(const NormPlan& p, int64_t rows) {
   const int64_t rpc = p.warps / p.row_warps, want = (rows + rpc - 1) / rpc, most = p.warps > 8 ? 148 : 148 * 2;
   return want < most ? want : most;
@@ -935,7 +934,7 @@ static int64_t norm_vjp_ctas(const NormPlan& p, int64_t rows) {
 size_t rms_norm_vjp_workspace_size(int64_t rows, int64_t K) {
   if (rows < 1 || K < 16 || K % 16 != 0 || K > kNormMaxK || product_exceeds(rows, K, kMaxElems)) return 0;
   const NormPlan p = norm_plan(K / 16, true);
-  return (size_t)norm_vjp_ctas(p, rows) * (p.warps / p.row_warps) * (size_t)K * 4;
+  return (size_t)norm_vjp_ctas(p, rows) * (size_t)K * 4;
 }
 
 nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
@@ -972,7 +971,7 @@ nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const fl
     const NormPlan p = norm_plan(K / 16, true);
     a.row_warps = p.row_warps;
     const int64_t ctas = norm_vjp_ctas(p, rows);
-    a.parts = (uint32_t)(ctas * (p.warps / p.row_warps));
+    a.parts = (uint32_t)ctas;
     dispatch_dt(dt, [&](auto tag_t) {
       using T = decltype(tag_t);
       if (!p.one) {
@@ -988,7 +987,7 @@ nvfp4_status rms_norm_vjp(const void* dy, const void* h, const void* w, const fl
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)((K + 31) / 32));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(norm::kDwThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
