@@ -574,7 +574,9 @@ NVFP4_API nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, 
  * only where its own bit is set), and the context, j < L - n, whole, or with a
  * window > 0 where j > L - n + depth - window, depth being the number of drafts
  * that query i sees less one, and at least 0: with masks of ancestors, the
- * query's place in its branch.  The window hides no drafts.
+ * query's place in its branch.  The window hides no drafts.  A draft that no
+ * query sees need not have been written (NVFP4: a block scale of NaN counts as
+ * 0 among the values here).
  * tree_mask [T, mask_words] uint32, a row for each query token;
  * 32*mask_words >= min(max_q, T), mask_words <= 2^20.  q_start is needed.
  * Everything else as in kv_attention. */

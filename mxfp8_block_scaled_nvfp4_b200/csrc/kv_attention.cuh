@@ -332,6 +332,12 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// e4m3 scale bytes with 0 for NaN.
+__device__ __forceinline__ uint32_t without_nan(uint32_t s) {
+  const uint32_t nan = ((s & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of each byte that is one
+  return s & ~((nan >> 7) * 255u);
+}
+
 // N scale bytes (N < 1: the byte that several lanes share).
 template <int N>
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
@@ -544,7 +550,8 @@ struct Decode {
   // O^T += V_hat^T . P^T of the tile at token `tok0`; fragment rows g and g + 8
   // of m-tile mt are elements (DP / 8) g + 2 mt and the next.  Bit i of `in`:
   // the lane's i-th token counts (what a masked place holds must not: P = 0
-  // does not hide a NaN).
+  // does not hide a NaN).  TREE: drafts that no mask names may hold anything.
+  template <bool TREE>
   __device__ __forceinline__ void weigh(const uint8_t* codes, const uint8_t* scales, uint32_t tok0, uint32_t in, const uint32_t (&ph)[NT][2],
                                         const uint32_t (&pl)[NT][2]) {
     uint32_t vw[4][G::vw], vs[4];
@@ -552,6 +559,7 @@ struct Decode {
     for (int i = 0; i < 4; ++i) {
       load_value(codes, scales, tok0 + token(2u * c + (i & 1)) + 8u * (i >> 1), vw[i], vs[i]);
       if (!((in >> i) & 1u)) vs[i] = 0;
+      if constexpr (TREE && MODE == kNV) vs[i] = without_nan(vs[i]);
     }
     if constexpr (MODE == kNV) {
 #pragma unroll
@@ -1076,7 +1084,7 @@ __global__ void __launch_bounds__(kDecThreads) k_kv_decode(const __grid_constant
             }
           }
         }
-        d.weigh(mem + v_at, mem + vs_at, tok0 + 16u * t, in[t], ph, pl);
+        d.template weigh<TREE>(mem + v_at, mem + vs_at, tok0 + 16u * t, in[t], ph, pl);
       }
       __syncwarp();
       if (lane == 0) arrive(shared_u32(&empty[st]));

@@ -167,12 +167,16 @@ struct Raw {
   // Decodes the slots into row `tok` of a tile, elements e0 .. e0 + EPT, as
   // 16-byte chunks: eight lanes (eight rows) cover eight chunk places.  up: of
   // the side (Mx).
+  // TREE: drafts that no mask names may hold anything, and P = 0 does not hide a
+  // NaN.
+  template <bool TREE>
   static __device__ __forceinline__ void decode(const AttnArgs& a, uint32_t at, uint32_t p, uint32_t first, bool there, uint32_t tile,
                                                 uint32_t tok, uint32_t e0, uint32_t up) {
     const uint32_t row = tile + (tok >> 3) * S::group + (tok & 7u) * 128u + (e0 >> 6) * 1024u, c0 = (e0 >> 3) & 7u;
     uint32_t s0, s1;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(at + S::raw_codes + 8u * p));
-    const uint32_t sc = there ? __funnelshift_r(s0, s1, 8u * first) : 0u;
+    uint32_t sc = there ? __funnelshift_r(s0, s1, 8u * first) : 0u;
+    if constexpr (TREE && MODE == kNV) sc = without_nan(sc);
 #pragma unroll
     for (int u = 0; u < units; ++u) {
       if (e0 + 32u * u >= a.D) break;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         break;
       }
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-      W::decode(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile,
+      W::template decode<TREE>(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile,
                 tok, e0, Mx<MODE>::up(side == 0));
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();

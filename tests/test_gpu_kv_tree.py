@@ -90,6 +90,31 @@ def test_masks_at_their_edges(nv, n, G):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("mode", ["nvfp4", "mxfp4", "mxfp8"])
+@pytest.mark.parametrize("n,G,D", [(6, 2, 64), (6, 2, 96), (9, 2, 256), (30, 4, 128), (60, 4, 64), (60, 4, 256)])
+def test_drafts_that_no_mask_names_hold_anything(nv, mode, n, G, D):
+    """Places of a tree that were never written: NaN scales, the largest ones
+    and infinities of every kind must not reach the queries."""
+    lens = [n + 70, n, 300]
+    c, t = make(nv, mode, lens, 2, D, 16, 3)
+    holes = [1, n // 2, n - 1]
+    dead = sum(1 << x for x in holes)
+    masks = [m & ~dead for b in range(3) for m in ancestors(n, b)]
+    q = seeded((3 * n + 2, 2 * G, D), 5, bf16)
+    want = compare_tree(nv, c, t, lens, [n] * 3, q, masks)
+    for fill in (0xFF, 0x7F, 0xFE, 0x7E):
+        for b, L in enumerate(lens):
+            for x in holes:
+                j = L - n + x
+                page, row = int(t[b, j // 16]), j % 16
+                for s in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+                    s.view(torch.uint8)[page, :, row] = fill
+        out, lse = torch.full(q.shape, 7.0, dtype=bf16, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+        nv.kv_attention_tree(c, q, t, i32(lens), pack(masks + [0, 0], 2).cuda(), i32(starts_of([n] * 3)), n, out=out, lse=lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    nv.check_device_errors()
+
+
 @pytest.mark.parametrize("mode", ["nvfp4", "mxfp8"])
 @pytest.mark.parametrize("n,G", [(3, 4), (16, 2), (64, 4)])
 def test_a_chain_is_causal_attention(nv, mode, n, G):
