@@ -394,13 +394,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
     constexpr int LOADS = 16 / RPI, NB = LOADS < 8 ? LOADS : 8;
     const uint32_t o = (uint32_t)lane % OPR;
     const float gk = a.g[0] ? __ldg(a.g[0]) / kGlobalEncode : 1.0f;
+    // n / G: the product with 2^32 / G is the quotient or one less
+    const uint32_t inv = a.G == 1u ? ~0u : (uint32_t)((1ull << 32) / a.G);
 #pragma unroll 1
     for (int k0 = 0; k0 < LOADS; k0 += NB) {
       uint4 raw[NB];
       const uint32_t rr0 = 16u * ((uint32_t)(warp - W_SOFT) & 7u) + RPI * k0 + (uint32_t)lane / OPR;
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        const uint32_t rq = min(r0 + 128u * qt + rr0 + RPI * k, R - 1u), i = rq / a.G, h = hk * a.G + (rq - i * a.G);
+        const uint32_t rq = min(r0 + 128u * qt + rr0 + RPI * k, R - 1u);
+        uint32_t i = __umulhi(rq, inv), h = rq - i * a.G;
+        if (h >= a.G) {
+          ++i;
+          h -= a.G;
+        }
+        h += hk * a.G;
         const QT* q = static_cast<const QT*>(a.q) + (int64_t)(s.t0 + i) * a.q_stride + (int64_t)h * a.D;
         raw[k] = o < a.D / 8u ? __ldg(reinterpret_cast<const uint4*>(q) + o) : make_uint4(0, 0, 0, 0);
       }
@@ -715,6 +723,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         if (!whole) a.part_ml[(uint64_t)chunk * a.T * a.Hq + at] = make_float2(m, l);
         else if (a.lse) a.lse[at] = lse_of(m, l);
       }
+      const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.part_o)) & 31u) == 0;
       // 16 columns at a time, in turn over the two or four threads that have the row
       for (uint32_t c = 16u * (dual ? 2 * qt + half : half); c < a.D; c += dual ? 64u : 32u) {
         uint32_t y[16];
@@ -732,17 +741,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
             for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f_mine + __uint_as_float(z[e]) * f_other);
           }
         }
-        if (r < R)
+        if (r < R) {
+          float v[2][8];
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[octet<MODE>(e)] = __uint_as_float(y[8 * o + e]) * f;
-            if (whole)
-              store8<QT>(static_cast<QT*>(a.out) + at * a.D + c + 8 * o, v);
-            else
-              store8<float>(a.part_o + ((uint64_t)chunk * a.T * a.Hq + at) * a.D + c + 8 * o, v);
+          for (int e = 0; e < 16; ++e) v[e / 8][octet<MODE>(e % 8)] = __uint_as_float(y[e]) * f;
+          if (whole) {
+            QT* o = static_cast<QT*>(a.out) + at * a.D + c;
+            if (wide) store16<QT, true>(o, v[0], v[1]);
+            else store16<QT, false>(o, v[0], v[1]);
+          } else {
+            float* o = a.part_o + ((uint64_t)chunk * a.T * a.Hq + at) * a.D + c;
+            if (wide) store16<float, true>(o, v[0], v[1]);
+            else store16<float, false>(o, v[0], v[1]);
           }
+        }
       }
     }
   }

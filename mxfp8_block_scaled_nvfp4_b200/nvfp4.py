@@ -804,7 +804,7 @@ def kv_cache_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.T
     dev, shape = _need_cache(cache), (T, heads, D)
     q_stride, k_stride, v_stride = _need_rows(q, (T, Hq, D), "q", dev), _need_rows(k, shape, "k", dev), _need_rows(v, shape, "v", dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dtype, device=cache.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     most, half = cos.shape
     _check(lib().kv_cache_append(cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), DT[dtype], T, Hq, q_stride, k_stride, v_stride,
                                  cos.data_ptr(), sin.data_ptr(), most, 2 * half, interleaved, positions.data_ptr(),
@@ -839,7 +839,7 @@ def kv_cache_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k_o
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=slots.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=slots.device)
+        v_out = torch.empty_like(k_out)
     if k_out.dtype != v_out.dtype or k_out.dtype not in DT:
         raise ValueError("k_out and v_out must share a dtype: float32, float16 or bfloat16")
     for t, what in ((k_out, "k_out"), (v_out, "v_out")):
@@ -902,7 +902,7 @@ def kv_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv_l
     if max_kv is None:
         max_kv = max_pages * cache.page_size
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     if workspace is None:
@@ -969,7 +969,7 @@ def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
     if max_kv is None:
         max_kv = max_pages * cache.page_size
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     if workspace is None:

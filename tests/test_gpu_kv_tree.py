@@ -168,6 +168,28 @@ def test_bad_sequences_and_pages(nv):
     nv.check_device_errors()
 
 
+@pytest.mark.parametrize("n,kv", [(8, 600), (20, 600), (64, 600), (64, 6000)])
+def test_outputs_and_queries_at_16_bytes(nv, n, kv):
+    """Rows that begin at 16 bytes and not at 32, of queries, results and partial results."""
+    G, D = 4, 128
+    c, t = make(nv, "nvfp4", [kv], 2, D, 64, 3)
+    q = seeded((n, 2 * G, D), 5, bf16)
+    mask = pack(ancestors(n, 1), 2).cuda()
+    size = nv.kv_attention_tree_workspace_size(1, n, 2 * G, 2, D, n, kv)
+    want = nv.kv_attention_tree(c, q, t, i32([kv]), mask, i32([0, n]), n, kv, return_lse=True)
+
+    def shifted(x, by):
+        s = torch.zeros(x.numel() + by, dtype=x.dtype, device="cuda")
+        s[by:] = x.reshape(-1)
+        return s[by:].view(x.shape)
+
+    out = shifted(torch.zeros_like(q), 8)
+    got = nv.kv_attention_tree(c, shifted(q, 8), t, i32([kv]), mask, i32([0, n]), n, kv, out=out, return_lse=True,
+                               workspace=torch.empty(size + 16, dtype=torch.uint8, device="cuda")[16:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    nv.check_device_errors()
+
+
 def test_many_sequences(nv):
     g = torch.Generator().manual_seed(1)
     B = 75
