@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant_
 // Bound by memory on many rows: 16384 x 8192 bf16 takes 169 us with its dw, 97 %
 // of the copy rate (a row at a time from registers 271, from shared memory two
 // rows ahead 202, two rows at a time 194, and with packed instructions and a
-// row's values kept from the first pass to the second, 18 instead of 34
+// row's values kept from the first pass to the second, 20 instead of 34
 // instructions an element, this).  2048 x 4096 takes 16.4 us for 7.7: seven rows
 // a CTA are a chain of four steps of 2 us, and dw is 3.4 us more.
 template <typename T>

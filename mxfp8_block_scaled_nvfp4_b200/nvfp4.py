@@ -932,7 +932,8 @@ def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
     [q_start[b] .. q_start[b + 1]) are the last of sequence b's kv_len[b] cached
     tokens, and each sees the context before them and of them those in its row
     of tree_mask [T, words] int32 (bit d % 32 of word d / 32: draft d, itself
-    included only where its bit is set; 32 * words >= max_q).  window: the
+    included only where its bit is set; 32 * words >= max_q, the host bound on a
+    sequence's drafts and by default as many as the masks hold).  window: the
     context within window tokens of the query's place in its branch (the number
     of drafts it sees, less one).  workspace: uint8 scratch of
     kv_attention_tree_workspace_size bytes (allocated here when None).  The rest
@@ -965,7 +966,7 @@ def kv_attention_tree(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
     if max_q is None:
-        max_q = T
+        max_q = min(T, 32 * tree_mask.shape[1])
     if max_kv is None:
         max_kv = max_pages * cache.page_size
     if out is None:
