@@ -576,7 +576,8 @@ NVFP4_API nvfp4_status kv_attention(const nvfp4_kv_cache* cache, const void* q, 
  * that query i sees less one, and at least 0: with masks of ancestors, the
  * query's place in its branch.  The window hides no drafts.  A draft that no
  * query sees need not have been written (NVFP4: a block scale of NaN counts as
- * 0 among the values here).
+ * 0 among the values here; among the keys it makes the queries that see the
+ * token NaN).
  * tree_mask [T, mask_words] uint32, a row for each query token;
  * 32*mask_words >= min(max_q, T), mask_words <= 2^20.  q_start is needed.
  * Everything else as in kv_attention. */

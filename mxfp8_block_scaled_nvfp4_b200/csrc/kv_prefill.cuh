@@ -166,17 +166,20 @@ struct Raw {
   }
   // Decodes the slots into row `tok` of a tile, elements e0 .. e0 + EPT, as
   // 16-byte chunks: eight lanes (eight rows) cover eight chunk places.  up: of
-  // the side (Mx).
-  // TREE: drafts that no mask names may hold anything, and P = 0 does not hide a
-  // NaN.
+  // the side (Mx).  values: of the values, where drafts that no mask names may
+  // hold anything (TREE), and P = 0 does not hide a NaN; what such a key gives is
+  // minus infinity before anything reads it, and a key that a query sees may
+  // make it NaN.
   template <bool TREE>
-  static __device__ __forceinline__ void decode(const AttnArgs& a, uint32_t at, uint32_t p, uint32_t first, bool there, uint32_t tile,
+  static __device__ __forceinline__ void decode(const AttnArgs& a, uint32_t at, uint32_t p, uint32_t first, bool there, bool values, uint32_t tile,
                                                 uint32_t tok, uint32_t e0, uint32_t up) {
     const uint32_t row = tile + (tok >> 3) * S::group + (tok & 7u) * 128u + (e0 >> 6) * 1024u, c0 = (e0 >> 3) & 7u;
     uint32_t s0, s1;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(at + S::raw_codes + 8u * p));
     uint32_t sc = there ? __funnelshift_r(s0, s1, 8u * first) : 0u;
-    if constexpr (TREE && MODE == kNV) sc = without_nan(sc);
+    if constexpr (TREE && MODE == kNV) {
+      if (values) sc = without_nan(sc);
+    }
 #pragma unroll
     for (int u = 0; u < units; ++u) {
       if (e0 + 32u * u >= a.D) break;
@@ -456,8 +459,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv_prefill(const __grid_constant
         break;
       }
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-      W::template decode<TREE>(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile,
-                tok, e0, Mx<MODE>::up(side == 0));
+      W::template decode<TREE>(a, sbase + S::at_raw + side * S::raw, p, cur & 3u, (cur & 4u) != 0, side != 0,
+                               sbase + (side ? S::at_v : S::at_k) + st * S::kv_tile, tok, e0, Mx<MODE>::up(side == 0));
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0 && !(side == 1 && warp == 0 && withheld_stage(n))) arrive(smem_u32(&full[side][st]));
