@@ -509,7 +509,7 @@ NVFP4_API nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* 
  * A move with a negative src or dst is skipped; one with a slot past the cache
  * is skipped and sets NVFP4_ERR_DEVICE_INDEX, as does a sequence whose starts
  * are not 0 <= starts[s] <= starts[s+1] <= M.
- * S*heads times a row's pieces (up to 34) below 2^31 (beyond:
+ * S*heads times a row's pieces (up to 42) below 2^31 (beyond:
  * NVFP4_ERR_UNSUPPORTED). */
 NVFP4_API nvfp4_status kv_cache_move(const nvfp4_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t M,
                                      const int32_t* starts, int64_t S, nvfp4_stream_t stream);
