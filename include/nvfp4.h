@@ -505,7 +505,9 @@ NVFP4_API nvfp4_status kv_cache_append(const nvfp4_kv_cache* cache, const void* 
  * starts [S+1] int32: moves starts[s] .. starts[s+1]-1 belong to sequence s and
  * take effect one after the other in that order, so accepted drafts can close
  * up in place; the slots that one sequence writes must not be among another's
- * slots.  NULL: S == M, every move is a sequence of its own.
+ * slots.  NULL: S == M, every move is a sequence of its own.  The moves of a
+ * sequence are one chain, eight at a time: copies without an order (a forked
+ * prefix) are many times faster with NULL.
  * A move with a negative src or dst is skipped; one with a slot past the cache
  * is skipped and sets NVFP4_ERR_DEVICE_INDEX, as does a sequence whose starts
  * are not 0 <= starts[s] <= starts[s+1] <= M.

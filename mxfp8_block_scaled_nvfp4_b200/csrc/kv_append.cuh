@@ -132,11 +132,11 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, uint32_t u) {
 
 // CTAs of Q first, then of K, then of V; of these a thread has 16 elements.
 // Bound by memory latency: slot and position, then the angles.  16384 tokens of
-// 32 query and 8 key/value heads of 128 to MXFP4, 64 elements turning: 71 us, 75
+// 32 query and 8 key/value heads of 128 to MXFP4, 64 elements turning: 71 us, 76
 // % of the copy rate (102 with a thread for every 16 elements of Q and its loads
-// behind the slot).  To NVFP4 with all 128 turning, one head a thread / four:
-// 64 tokens 2.8 / 3.0 us, 1024 5.9 / 5.4 (5.9 / 6.1 in neighbouring pairs), 2048
-// 14.6 / 12.2, 16384 96 / 75.
+// behind the slot).  To NVFP4 with all 128 turning, 74 % of it: 74 us, and one
+// head a thread / four: 64 tokens 2.8 / 3.0 us, 1024 5.9 / 5.4 (5.9 / 6.1 in
+// neighbouring pairs), 2048 14.6 / 12.2, 16384 96 / 75.
 template <typename T, int MODE, bool V8, int HEADS>
 __global__ void __launch_bounds__(kRowThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
   if (blockIdx.x < a.q_ctas) {
@@ -219,8 +219,9 @@ __device__ __forceinline__ void store_piece(uint8_t* p, uint32_t bytes, const ui
 }
 
 // Bound by memory latency (the indices, then the rows): 32000 rows of 8 x 128 in
-// MXFP8 29 us, 71 % of the copy rate (118 through the ordered kernel, a sequence
-// a move).
+// MXFP8 29 us, 71 % of the copy rate.  Through the ordered kernel, whose threads
+// take a sequence's moves eight at a time: 105 as 32000 sequences, 34 as 1000 of
+// 32, 707 as 32 of 1000.
 template <bool ORDERED>
 __global__ void __launch_bounds__(kRowThreads) k_kv_move(const __grid_constant__ MoveArgs a) {
   const uint32_t u = blockIdx.x * kRowThreads + threadIdx.x;

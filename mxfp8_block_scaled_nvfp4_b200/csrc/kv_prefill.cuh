@@ -25,7 +25,7 @@
 // transpose.
 //
 // Measured: 4096 queries over 8192 tokens (NVFP4, 32 / 8 heads of 128, causal)
-// 505 us, 816 TFLOP/s or 49 % of the bf16 burst rate, at an SM clock of 1.83 GHz
+// 503 us, 819 TFLOP/s or 49 % of the bf16 burst rate, at an SM clock of 1.83 GHz
 // (by the SMs' own counter; 970 W).  With 148 CTAs of two query tiles, a tile of
 // 128 tokens takes 2.78 us, about 5000 clocks for 2048 of products (MXFP4 3.38,
 // MXFP8 3.95, which have half as many products again), and a CTA 11 us besides:
@@ -69,8 +69,8 @@ struct Shape {
 };
 
 // Through L1, unlike copy16: a thread's 16-byte pieces are parts of lines that
-// its neighbours read too (2048 over 4096 tokens MXFP8 217 us, past L1 228;
-// MXFP4 181 and 184; 4096 over 8192 NVFP4 528 and 526).
+// its neighbours read too (2048 over 4096 tokens MXFP8 204 us, past L1 214;
+// MXFP4 170 and 173, NVFP4 139 and 141; 4096 over 8192 NVFP4 503 and 499).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

@@ -208,7 +208,9 @@ __device__ __forceinline__ void put_scales(const ScaleOut& so, uint32_t row, uin
 // A row's warps are one CTA's (several rows a CTA where they are short), so a
 // row's sum is one barrier, and the row is read once.  16384 x 8192 bf16 with a
 // residual to MXFP8 takes 146 us, 99 % of the copy rate; 4096 x 4096 to NVFP4 21
-// us (5.2 TB/s), with half of the issue slots used; one row of 4096 2.4 us.
+// us (5.2 TB/s), with half of the issue slots used; one row of 4096 2.3 us.  With
+// four blocks a thread 4096 x 16384 to NVFP4 109 us for 67; rows that leave lanes
+// without a block, 131072 x 128, 71 for 17 (as plain output 51 for 20.5).
 template <typename T, int OUT, int U>
 __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant__ Args a) {
   constexpr bool kAhead = U == 1, V8 = U == 1;
@@ -308,14 +310,15 @@ __global__ void __launch_bounds__(kMaxThreads) k_rms_norm(const __grid_constant_
 // of 16 elements, K <= 8192): R rows at a time are copied into shared memory a
 // step ahead, each thread's pieces into slots of its own, so that no barrier
 // stands between copy and use; longer rows are read twice.
-// Bound by memory on many rows: 16384 x 8192 bf16 takes 169 us with its dw, 97 %
+// Bound by memory on many rows: 16384 x 8192 bf16 takes 168 us with its dw, 97 %
 // of the copy rate (a row at a time from registers 271, from shared memory two
 // rows ahead 202, two rows at a time 194, and with packed instructions and a
 // row's values kept from the first pass to the second, 20 instead of 34
-// instructions an element, this).  2048 x 4096 takes 16.4 us for 7.7: seven rows
-// a CTA are a chain of four steps of 2 us, and dw is 3.4 us more.
+// instructions an element, this).  2048 x 4096 takes 16 us for 7.7: seven rows
+// a CTA are a chain of four steps of 2 us, and dw is 3.4 us more.  Rows read
+// twice: 4096 x 16384 175 us for 82.
 template <typename T>
-constexpr int kVjpRows = sizeof(T) == 4 ? 1 : 2;  // in shared memory: two steps of 48 KB a row and stage
+constexpr int kVjpRows = sizeof(T) == 4 ? 1 : 2;  // of a step: at K 8192 two stages of 96 KB, 48 KB a row (fp32 96)
 template <typename T>
 constexpr uint32_t kVjpSmem = 2 * kVjpRows<T> * 3 * 16 * sizeof(T);  // bytes a thread
 

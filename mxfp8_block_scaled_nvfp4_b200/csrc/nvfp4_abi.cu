@@ -1265,8 +1265,10 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   p.prefill = prefill_has_it && rows > (D <= 64 ? 48 : D <= 128 ? 32 : 16);
   p.chunk = p.chunks = 1;
   if (!p.prefill) {
-    // D 256: two n-tiles would take more registers than there are; trees of so
-    // few rows are rare and have no variant of their own
+    // D 256: two n-tiles would take more registers than there are.  Trees of at
+    // most 8 rows have no variant of their own (24 kernels more): with one, 1 x 2
+    // drafts of group 4 over 8192 tokens take 16.4 us for 15.9, 16 of them 46 for
+    // 75, and 64 145 for 264 (NVFP4; MXFP4 209 for 417, MXFP8 256 for 469).
     p.tile_rows = (rows <= 8 && !tree) || D > 128 ? 8 : 16;
     p.bytes_per_chunk = (size_t)(2 * p.tile_rows * (D * 4 + 8) + 32);
     return p;
@@ -1283,8 +1285,13 @@ static KvPlan kv_plan(int64_t B, int64_t T, int64_t Hq, int64_t heads, int64_t D
   if (fit < 2) fit = 1;
   if (tree) {
     // Few row tiles: as many chunks as take the least time, in tiles of 128
-    // tokens (2.8 us): a CTA costs 5 of them besides its own, the join 3.  (144
-    // row tiles over 4160 tokens: 113 us whole, 186 in chunks of 4096.)
+    // tokens: a CTA costs 5 of them besides its own, the join 3.  (144 row tiles
+    // over 4160 tokens: 106 us whole, 178 in two chunks.)  That holds for NVFP4,
+    // D 128 and two query tiles (2.8 us a tile, 15 a call of one wave besides); a
+    // tile is 1.5 to 5.3 us over formats, head sizes and one query tile, and the
+    // rest 3 to 6.6 of them.  So flat is the minimum that the choice is within 2 %
+    // of the best of 12 numbers of chunks all the same (NVFP4 and MXFP8, D 64, 128
+    // and 256, 1 to 12 trees of 32 and 64 drafts over 2048 to 65536 tokens).
     double best = 0;
     for (int64_t c = 1; c <= 64 && c <= fit && (c - 1) * 128 < (span > 0 ? span : 1); ++c) {
       const int64_t each = ((span + c - 1) / c + 127) / 128;

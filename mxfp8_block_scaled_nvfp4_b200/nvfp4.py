@@ -815,8 +815,9 @@ def kv_cache_append(cache: KvCache, q: torch.Tensor, k: torch.Tensor, v: torch.T
 def kv_cache_move(cache: KvCache, src: torch.Tensor, dst: torch.Tensor, starts: torch.Tensor | None = None) -> None:
     """Copy the rows of slots src [M] to slots dst [M] (int32; a negative one
     skips its move).  starts [S + 1] int32: the moves starts[s] .. starts[s + 1]
-    - 1 of a sequence take effect one after the other; None: every move for
-    itself (no slot is then both written and read or written twice)."""
+    - 1 of a sequence take effect one after the other, as a chain; None: every
+    move for itself (no slot is then both written and read or written twice),
+    many times faster for long copies."""
     M = src.shape[0]
     _need_dtype(src, torch.int32, "src")
     _need_dtype(dst, torch.int32, "dst")
